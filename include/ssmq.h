@@ -76,7 +76,11 @@ typedef enum {
                                  the limit of ssmq_quantize_groups' pipeline waits;
                                  0 makes them give up at once. */
 
-typedef enum { SSMQ_F32 = 0, SSMQ_F16 = 1 } ssmq_dtype;
+typedef enum {
+  SSMQ_F32 = 0,
+  SSMQ_F16 = 1,
+  SSMQ_BF16 = 2 /* the quantized-layer operators and the gated scan only */
+} ssmq_dtype;
 typedef enum { SSMQ_SCALE_STATIC = 0, SSMQ_SCALE_ABSMAX = 1 } ssmq_scale_mode;
 typedef enum {
   SSMQ_X_INT8_GROUP = 0,   /* int8 codes, one fp32 scale per channel cluster */
@@ -663,6 +667,150 @@ typedef struct {
 } ssmq_m1_decode_args;
 
 ssmq_status ssmq_selective_state_update_w8(const ssmq_m1_decode_args* args, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Quantized layer: norm + codes, int8 matrix product                         */
+/* ------------------------------------------------------------------------ */
+/*
+ * Passage: Quamba2 abstract (W8A8: 8-bit weights and 8-bit activations around
+ * the recurrence).  The two calls are the layer's entry and its projections:
+ * the residual stream is normalised and coded once per token, and the codes
+ * are multiplied with int8 weights.
+ *
+ * The calls below take SSMQ_F32, SSMQ_F16 and SSMQ_BF16 tensors whose last
+ * dimension is contiguous and whose rows lie `stride` elements apart (stride
+ * >= the row's length), so that column slices of a wider tensor need no copy.
+ * Base pointers need the alignment of one element (tensors without a stride
+ * argument: 4 bytes for fp32 and int32); rows on 16-byte boundaries take
+ * vectorised paths with the same results.
+ */
+
+/*
+ * ssmq_rms_norm_quantize: per token t (a row of `dim` channels)
+ *   r = x + residual, rounded once to dtype (r = x without a residual)
+ *   ms = sum_c r_c^2 / dim in binary32, rstd = 1 / sqrt(ms + eps)
+ *   v_c = fl32(fl32(r_c weight_c) rstd)
+ *   scales[t] = fl32(max_c |v_c| / 127)
+ *   codes[t][c] = clamp(round_half_even(fl32(v_c / scales[t])), -127, 127)
+ * (the codes of ssmq_quantize_groups with one group per token).  A zero scale
+ * codes its token as 0.  A token whose sum of squares is not finite (an
+ * infinite or NaN element, or an overflow) gets scale 0 and codes 0, and an
+ * element that is not finite for its weight's sake is coded 0 and left out of
+ * the maximum; both set SSMQ_DEV_NONFINITE.
+ *
+ * x            (tokens, dim), x_stride; residual the same, or NULL
+ * weight       fp32[dim] or NULL (ones)
+ * residual_out r, (tokens, dim), or NULL; may be exactly x or residual (same
+ *              address and stride), otherwise overlaps neither
+ * y            v rounded to dtype, (tokens, dim), or NULL; overlaps no input
+ * codes        int8 (tokens, dim), codes_stride bytes apart; NULL with NULL
+ *              scales leaves the codes out (then y is required)
+ * scales       fp32[tokens]
+ * Bytes between a row's end and the next row are not written.
+ * Supported: 1 <= dim <= 32768.  Errors: INVALID_ARG (NULL, sizes, strides,
+ * overlaps, eps negative or NaN), UNSUPPORTED (dim), ALIGNMENT.
+ */
+typedef struct {
+  int64_t tokens, dim;
+  int32_t dtype;            /* ssmq_dtype of x, residual, residual_out and y */
+  float eps;
+  const void* x;
+  int64_t x_stride;
+  const void* residual;
+  int64_t residual_stride;
+  const float* weight;
+  void* residual_out;
+  int64_t residual_out_stride;
+  void* y;
+  int64_t y_stride;
+  int8_t* codes;
+  int64_t codes_stride;
+  float* scales;
+  uint32_t* status;
+} ssmq_norm_args;
+
+ssmq_status ssmq_rms_norm_quantize(const ssmq_norm_args* args, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Gated linear recurrence                                                    */
+/* ------------------------------------------------------------------------ */
+/*
+ * Passage: the linear recurrence of the Quamba2 abstract with the decay given
+ * directly by a per-channel forget gate and a tied input gate (the pages name
+ * no such layer; it is the same recurrence h_t = a_t h_{t-1} + u_t with a
+ * scalar state per channel):
+ *   f_t = sigmoid(g_t),  h_t = f_t h_{t-1} + (1 - f_t) v_t
+ *   y_t = h_t             without z
+ *   y_t = h_t silu(z_t)   with z
+ * Gates, states and sums are binary32 (1 - f_t is formed as sigmoid(-g_t), not
+ * by subtraction); y and the gradients are rounded once to dtype.  g = -inf
+ * forgets the state (f = 0: a new sequence starts), g = +inf keeps it and
+ * ignores a finite v.  A non-finite v or state makes the later states of its
+ * channel non-finite.
+ *
+ * Layouts (b = batch, L = seqlen, d = dim): v, g, z, y, dy, dv, dg, dz are
+ * (b, L, d) of dtype, element (i, t, c) at i * batch_stride + t * row_stride + c
+ * (row_stride >= d unless L is 1; batch_stride >= 0, for an output large
+ * enough that sequences do not overlap).  h0, h_final, dh0, dh_final: fp32
+ * (b, d), dense; NULL h0 / dh_final: zeros.  h_final may be h0 and dh0 may be
+ * dh_final (the same address).
+ * lengths: device int32[b] or NULL.  Sequence i has lengths[i] steps (values
+ * outside [0, L] are read as the nearest end); its other rows are not read, y
+ * and the gradients there are 0, and h_final is the state after its last step
+ * (h0 for a length of 0).
+ *
+ * ssmq_gated_scan: y (required) and, when given, h_final and states: fp32
+ *   (b, ceil(L / S), d), the state before every S-th step (S =
+ *   ssmq_gated_scan_state_steps()), which the gradient reads.  y may be
+ *   exactly z (same address and strides) or overlap no input.
+ * ssmq_gated_scan_backward: gradients of sum(dy y) + sum(dh_final h_final)
+ *   by the recurrence run backwards: with l_t = dy_t silu(z_t) + f_{t+1} l_{t+1}
+ *   (dh_final added at the last step),
+ *   dv = (1 - f) l, dg = f (1 - f) (h_{t-1} - v) l, dz = dy h silu'(z),
+ *   dh0 = f_0 l_0.  v, g, z, lengths and states are those of the forward
+ *   call.  dv, dg (and dz with z) are required, dh0 optional; each may be
+ *   exactly one of v, g, z, dy (same address and strides; no two the same),
+ *   otherwise they overlap nothing.
+ * ssmq_gated_update: one step in place on state (fp32 (b, d), dense); seqlen
+ *   is 1 and only the batch strides count.  y may be exactly z.
+ *
+ * The order of every sum depends on the sizes alone: a call repeated on the
+ * same inputs gives the same bytes.  No workspace; any L >= 0, any d.
+ * Errors: INVALID_ARG (NULL, negative sizes, bad strides, overlaps),
+ * ALIGNMENT (base not on an element), UNSUPPORTED (b * ceil(d / 16) > 2^27).
+ */
+typedef struct {
+  void* p;                  /* device, NULL where the tensor is absent */
+  int64_t batch_stride, row_stride; /* in elements */
+} ssmq_rows;
+
+typedef struct {
+  int64_t batch, seqlen, dim;
+  int32_t dtype;
+  ssmq_rows v, g, z;        /* inputs; z.p NULL: no output gate */
+  ssmq_rows y;
+  const float* h0;
+  float* h_final;
+  float* states;
+  const int32_t* lengths;
+} ssmq_gated_args;
+
+typedef struct {
+  int64_t batch, seqlen, dim;
+  int32_t dtype;
+  ssmq_rows v, g, z, dy;
+  ssmq_rows dv, dg, dz;
+  const float* states;
+  const float* dh_final;
+  float* dh0;
+  const int32_t* lengths;
+} ssmq_gated_grad_args;
+
+int32_t ssmq_gated_scan_state_steps(void);
+ssmq_status ssmq_gated_scan(const ssmq_gated_args* args, void* stream);
+ssmq_status ssmq_gated_scan_backward(const ssmq_gated_grad_args* args, void* stream);
+/* args: h0 is not read, h_final is the state (in and out), states must be NULL */
+ssmq_status ssmq_gated_update(const ssmq_gated_args* args, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Diagnostics                                                               */

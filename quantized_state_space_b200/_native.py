@@ -17,7 +17,7 @@ STATUS_NAMES = {0: "SSMQ_OK", 1: "SSMQ_ERR_INVALID_ARG", 2: "SSMQ_ERR_ALIGNMENT"
                 3: "SSMQ_ERR_UNSUPPORTED", 4: "SSMQ_ERR_CUDA", 5: "SSMQ_ERR_TIMEOUT",
                 6: "SSMQ_ERR_NONFINITE"}
 DEV_NONFINITE, DEV_BAD_GROUP, DEV_BAD_SCALE, DEV_TIMEOUT = 1, 2, 4, 8
-F32, F16 = 0, 1
+F32, F16, BF16 = 0, 1, 2
 SCALE_STATIC, SCALE_ABSMAX = 0, 1
 X_INT8_GROUP, X_SOFTEDGE, X_F16_GROUP, X_F16_SOFTEDGE = 0, 1, 2, 3
 
@@ -82,6 +82,32 @@ class ConvArgs(C.Structure):
                 ("u", _vp), ("x_prev_out", _vp), ("status", _vp)]
 
 
+class NormArgs(C.Structure):
+    _fields_ = [("tokens", _i64), ("dim", _i64), ("dtype", _i32), ("eps", _f32), ("x", _vp),
+                ("x_stride", _i64), ("residual", _vp), ("residual_stride", _i64),
+                ("weight", _vp), ("residual_out", _vp), ("residual_out_stride", _i64),
+                ("y", _vp), ("y_stride", _i64), ("codes", _vp), ("codes_stride", _i64),
+                ("scales", _vp), ("status", _vp)]
+
+
+def _rows(name):
+    """The fields of one ssmq_rows member (pointer and strides), flattened."""
+    return [(name, _vp), (name + "_batch_stride", _i64), (name + "_row_stride", _i64)]
+
+
+class GatedArgs(C.Structure):
+    _fields_ = [("batch", _i64), ("seqlen", _i64), ("dim", _i64), ("dtype", _i32),
+                *_rows("v"), *_rows("g"), *_rows("z"), *_rows("y"), ("h0", _vp),
+                ("h_final", _vp), ("states", _vp), ("lengths", _vp)]
+
+
+class GatedGradArgs(C.Structure):
+    _fields_ = [("batch", _i64), ("seqlen", _i64), ("dim", _i64), ("dtype", _i32),
+                *_rows("v"), *_rows("g"), *_rows("z"), *_rows("dy"), *_rows("dv"), *_rows("dg"),
+                *_rows("dz"), ("states", _vp), ("dh_final", _vp), ("dh0", _vp),
+                ("lengths", _vp)]
+
+
 # entry point -> (restype, argtypes); every name declared in include/ssmq.h
 class QuantJob(C.Structure):
     _fields_ = [("src", _vp), ("dtype", _i32), ("outer", _i64), ("mid", _i64), ("inner", _i64),
@@ -116,6 +142,11 @@ SIGNATURES = {
                                            _vp]),
     "ssmq_softedge_calibrate_noalloc": (_i32, [_vp, _i32, _i64, C.c_double, C.c_double, _f32,
                                                _vp, _vp]),
+    "ssmq_rms_norm_quantize": (_i32, [C.POINTER(NormArgs), _vp]),
+    "ssmq_gated_scan_state_steps": (_i32, []),
+    "ssmq_gated_scan": (_i32, [C.POINTER(GatedArgs), _vp]),
+    "ssmq_gated_scan_backward": (_i32, [C.POINTER(GatedGradArgs), _vp]),
+    "ssmq_gated_update": (_i32, [C.POINTER(GatedArgs), _vp]),
     "ssmq_probe_ex2": (_i32, [_i32, _vp, C.POINTER(C.c_int64), _vp]),
     "ssmq_last_error": (C.c_char_p, []),
     "ssmq_version": (_i32, []),
@@ -278,6 +309,44 @@ def ssmq_ssd_carry_in(h_carry, workspace=None, ws_bytes=0, stream=None, **fields
 def ssmq_state_chain(h_end, dec, n_parts, units, elems, h_out, stream=None):
     _check(lib().ssmq_state_chain(ptr(h_end), ptr(dec), n_parts, units, elems, ptr(h_out),
                                   _stream(stream)))
+
+
+def _struct(cls, fields):
+    """An argument struct from keywords; unlike _fill, tensors become addresses
+    in one pass and the struct's own constructor checks the names."""
+    for k, v in fields.items():
+        if hasattr(v, "data_ptr"):
+            fields[k] = v.data_ptr()
+    return cls(**fields)
+
+
+def ssmq_rms_norm_quantize(stream=None, **fields):
+    """Fields of ssmq_norm_args as keywords (tensors for pointer fields)."""
+    a = _struct(NormArgs, fields)
+    _check(lib().ssmq_rms_norm_quantize(C.byref(a), _stream(stream)))
+
+
+def ssmq_gated_scan_state_steps():
+    return int(lib().ssmq_gated_scan_state_steps())
+
+
+def ssmq_gated_scan(stream=None, **fields):
+    """Fields of ssmq_gated_args as keywords; the strides of tensor x are
+    x_batch_stride and x_row_stride."""
+    a = _struct(GatedArgs, fields)
+    _check(lib().ssmq_gated_scan(C.byref(a), _stream(stream)))
+
+
+def ssmq_gated_scan_backward(stream=None, **fields):
+    """Fields of ssmq_gated_grad_args as keywords (strides as ssmq_gated_scan)."""
+    a = _struct(GatedGradArgs, fields)
+    _check(lib().ssmq_gated_scan_backward(C.byref(a), _stream(stream)))
+
+
+def ssmq_gated_update(stream=None, **fields):
+    """Fields of ssmq_gated_args as keywords; h_final is the state."""
+    a = _struct(GatedArgs, fields)
+    _check(lib().ssmq_gated_update(C.byref(a), _stream(stream)))
 
 
 def ssmq_state_update_w8(stream=None, **fields):

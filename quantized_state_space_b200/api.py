@@ -50,7 +50,7 @@ def _in(t, name, dtypes, numel, device):
 def _on(device):
     """Launches go to the device that holds the tensors (and its current
     stream), whatever device is current in the caller."""
-    if device.type == "cuda":
+    if device.type == "cuda" and device.index != torch.cuda.current_device():
         return torch.cuda.device(device)
     return contextlib.nullcontext()
 
@@ -618,3 +618,237 @@ def softedge_calibrate_noalloc(src, thresholds, *, q_lo=5.0, q_hi=99.9, alpha=1.
     with _on(src.device):
         N.ssmq_softedge_calibrate_noalloc(src, src.numel(), q_lo, q_hi, alpha, thresholds)
     return thresholds
+
+
+# ---- quantized layer: norm + codes, int8 matrix product ----------------------
+
+_DTYPE_IDS = {torch.float32: N.F32, torch.float16: N.F16, torch.bfloat16: N.BF16}
+
+
+def _row_tensor(t, name, shape, dtype, device):
+    """A tensor of contiguous rows (..., d) for the strided-row operators: of
+    this shape, dtype and device, its last dimension contiguous."""
+    if t.device != device or device.type != "cuda":
+        raise ValueError("%s must be a CUDA tensor on %s" % (name, device))
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError("%s must be %s of shape %s (got %s of %s)"
+                         % (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError("%s: the last dimension must be contiguous" % name)
+
+
+def _flat_rows(t, name, shape, dtype, device):
+    """(address, row stride) of a (..., d) tensor seen as (tokens, d): the
+    leading dimensions must merge into one with a constant stride."""
+    _row_tensor(t, name, shape, dtype, device)
+    if t.is_contiguous():
+        return t.data_ptr(), shape[-1]
+    stride, span = None, 0
+    for size, st in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if stride is None:
+            stride, span = st, st * size
+        elif st != span:
+            raise ValueError("%s: the rows must lie a constant stride apart" % name)
+        else:
+            span = st * size
+    return t.data_ptr(), shape[-1] if stride is None else stride
+
+
+def rms_norm_quantize(x, weight=None, *, residual=None, eps=1e-5, residual_out=None,
+                      want_codes=True, codes=None, scales=None, want_y=False, y=None,
+                      status=None):
+    """Residual add + root-mean-square norm + int8 codes, one scale a token.
+
+    x, residual (..., d) float16 / bfloat16 / float32, rows a constant stride
+    apart; weight (d,) float32 or None.  Returns (codes, scales), plus r =
+    x + residual (in x's dtype) when residual is given, plus the normalised
+    values (in x's dtype) when want_y.  codes (..., d) int8 and scales (...)
+    float32 feed int8_linear.  residual_out may be x or residual itself (in
+    place).  want_codes=False leaves the codes out (codes and scales are then
+    None).  Codes that the call allocates lie on 16-byte rows."""
+    d = x.shape[-1]
+    dv, dt = x.device, x.dtype
+    if dt not in _DTYPE_IDS:
+        raise ValueError("x must be float16, bfloat16 or float32 (got %s)" % dt)
+    shape, lead = x.shape, x.shape[:-1]
+    xp, xs = _flat_rows(x, "x", shape, dt, dv)
+    tokens = 1
+    for v in lead:
+        tokens *= v
+    _in(weight, "weight", torch.float32, d, dv)
+    _status(status, dv)
+    with _on(dv):
+        f = dict(tokens=tokens, dim=d, dtype=_DTYPE_IDS[dt], eps=eps, x=xp, x_stride=xs,
+                 weight=weight, status=status)
+        out = ()
+        if residual is not None:
+            f["residual"], f["residual_stride"] = _flat_rows(residual, "residual", shape, dt, dv)
+            if residual_out is None:
+                residual_out = torch.empty(shape, dtype=dt, device=dv)
+            out = (residual_out,)
+        if residual_out is not None:
+            f["residual_out"], f["residual_out_stride"] = _flat_rows(residual_out, "residual_out",
+                                                                     shape, dt, dv)
+        if want_y or y is not None:
+            if y is None:
+                y = torch.empty(shape, dtype=dt, device=dv)
+            f["y"], f["y_stride"] = _flat_rows(y, "y", shape, dt, dv)
+            out += (y,)
+        if want_codes or codes is not None or scales is not None:
+            if codes is None:
+                codes = torch.empty((*lead, (d + 15) // 16 * 16), dtype=torch.int8, device=dv)
+                if d % 16:
+                    codes = codes[..., :d]
+            if scales is None:
+                scales = torch.empty(lead, dtype=torch.float32, device=dv)
+            _out(scales, "scales", torch.float32, tokens, dv)
+            f["codes"], f["codes_stride"] = _flat_rows(codes, "codes", shape, torch.int8, dv)
+            f["scales"] = scales
+        N.ssmq_rms_norm_quantize(torch.cuda.current_stream().cuda_stream, **f)
+    return (codes, scales) + out
+
+
+# ---- gated linear recurrence ----------------------------------------------------
+
+def _gated_rows(f, t, name, shape, dtype, device):
+    """Address and strides of a (b, L, d) tensor into the call's fields."""
+    _row_tensor(t, name, shape, dtype, device)
+    st = t.stride()
+    f[name] = t.data_ptr()
+    f[name + "_batch_stride"] = st[0]
+    f[name + "_row_stride"] = st[1]
+
+
+def _gated_scan(v, g, z, h0, lengths, y, h_final, states, return_state, save_states):
+    if v.dim() != 3 or v.dtype not in _DTYPE_IDS:
+        raise ValueError("v must be a (b, L, d) float16, bfloat16 or float32 tensor")
+    shape, dv, dt = v.shape, v.device, v.dtype
+    b, L, d = shape
+    _in(h0, "h0", torch.float32, b * d, dv)
+    _in(lengths, "lengths", torch.int32, b, dv)
+    f = dict(batch=b, seqlen=L, dim=d, dtype=_DTYPE_IDS[dt], h0=h0, lengths=lengths)
+    _gated_rows(f, v, "v", shape, dt, dv)
+    _gated_rows(f, g, "g", shape, dt, dv)
+    if z is not None:
+        _gated_rows(f, z, "z", shape, dt, dv)
+    with _on(dv):
+        if y is None:
+            y = torch.empty(shape, dtype=dt, device=dv)
+        _gated_rows(f, y, "y", shape, dt, dv)
+        if h_final is None and return_state:
+            h_final = torch.empty((b, d), dtype=torch.float32, device=dv)
+        _out(h_final, "h_final", torch.float32, b * d, dv)
+        if save_states or states is not None:
+            k = N.ssmq_gated_scan_state_steps()
+            n = (L + k - 1) // k
+            if states is None:
+                states = torch.empty((b, n, d), dtype=torch.float32, device=dv)
+            _out(states, "states", torch.float32, b * n * d, dv)
+        f["h_final"], f["states"] = h_final, states
+        N.ssmq_gated_scan(torch.cuda.current_stream().cuda_stream, **f)
+    return y, h_final, states
+
+
+class _GatedScan(torch.autograd.Function):
+    """The scan with its gradient, for inputs that require one."""
+
+    @staticmethod
+    def forward(ctx, v, g, z, h0, lengths):
+        y, h_final, states = _gated_scan(v, g, z, h0, lengths, None, None, None, True, True)
+        ctx.save_for_backward(v, g, z, lengths, states)
+        return y, h_final
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dh_final):
+        v, g, z, lengths, states = ctx.saved_tensors
+        if dy.stride(-1) != 1 or (v.shape[1] > 1 and dy.stride(1) < v.shape[2]):
+            dy = dy.contiguous()  # (an expanded gradient, as of a sum)
+        dv, dg, dz, dh0 = gated_scan_backward(dy.to(v.dtype), v, g, states, z=z,
+                                              dh_final=dh_final.contiguous(), lengths=lengths)
+        return dv, dg, dz, dh0 if ctx.needs_input_grad[3] else None, None
+
+
+def gated_scan(v, g, *, z=None, h0=None, lengths=None, y=None, h_final=None, states=None,
+               return_state=True, save_states=False):
+    """Gated linear recurrence h_t = f_t h_{t-1} + (1 - f_t) v_t, f =
+    sigmoid(g), y_t = h_t or h_t silu(z_t).
+
+    v, g, z (b, L, d) float16 / bfloat16 / float32 with contiguous channels
+    (column slices of a projection's output need no copy); h0 (b, d) float32
+    or None; lengths (b,) int32 or None: the steps of each sequence (rows
+    behind them give y = 0 and leave the state).  Returns (y, h_final), or (y,
+    h_final, states) with save_states: the states that gated_scan_backward
+    reads (or that are written into ``states`` when it is given).  When an
+    input requires a gradient, the result is differentiable; the caller's
+    output tensors are then not accepted."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (v, g, z, h0)):
+        if not (y is None and h_final is None and states is None and not save_states):
+            raise ValueError("y, h_final, states and save_states are for inputs without "
+                             "requires_grad")
+        out, h = _GatedScan.apply(v, g, z, h0, lengths)
+        return out, (h if return_state else None)
+    y, h_final, states = _gated_scan(v, g, z, h0, lengths, y, h_final, states, return_state,
+                                     save_states)
+    return (y, h_final, states) if states is not None else (y, h_final)
+
+
+def gated_scan_backward(dy, v, g, states, *, z=None, dh_final=None, lengths=None, dv=None,
+                        dg=None, dz=None, dh0=None):
+    """Gradients (dv, dg, dz, dh0) of a gated_scan call with save_states: dy
+    (b, L, d) and dh_final (b, d) float32 or None are the gradients of its
+    outputs; dz is None without z.  Outputs may be given; dv, dg and dz may be
+    exactly v, g, z or dy (each a different one)."""
+    if v.dim() != 3 or v.dtype not in _DTYPE_IDS:
+        raise ValueError("v must be a (b, L, d) float16, bfloat16 or float32 tensor")
+    shape, dvc, dt = v.shape, v.device, v.dtype
+    b, L, d = shape
+    k = N.ssmq_gated_scan_state_steps()
+    _in(states, "states", torch.float32, b * ((L + k - 1) // k) * d, dvc)
+    _in(dh_final, "dh_final", torch.float32, b * d, dvc)
+    _in(lengths, "lengths", torch.int32, b, dvc)
+    _out(dh0, "dh0", torch.float32, b * d, dvc)
+    f = dict(batch=b, seqlen=L, dim=d, dtype=_DTYPE_IDS[dt], states=states, dh_final=dh_final,
+             lengths=lengths)
+    if z is None and dz is not None:
+        raise ValueError("dz without z")
+    with _on(dvc):
+        if dv is None:
+            dv = torch.empty(shape, dtype=dt, device=dvc)
+        if dg is None:
+            dg = torch.empty(shape, dtype=dt, device=dvc)
+        if z is not None and dz is None:
+            dz = torch.empty(shape, dtype=dt, device=dvc)
+        if dh0 is None:
+            dh0 = torch.empty((b, d), dtype=torch.float32, device=dvc)
+        f["dh0"] = dh0
+        for t, name in ((v, "v"), (g, "g"), (z, "z"), (dy, "dy"), (dv, "dv"), (dg, "dg"),
+                        (dz, "dz")):
+            if t is not None:
+                _gated_rows(f, t, name, shape, dt, dvc)
+        N.ssmq_gated_scan_backward(torch.cuda.current_stream().cuda_stream, **f)
+    return dv, dg, dz, dh0
+
+
+def gated_update(state, v, g, *, z=None, y=None):
+    """One step of the gated recurrence in place on ``state`` (b, d) float32;
+    v, g, z (b, d) with contiguous channels.  Returns y (b, d) in v's dtype
+    (y may be z itself)."""
+    if v.dim() != 2 or v.dtype not in _DTYPE_IDS:
+        raise ValueError("v must be a (b, d) float16, bfloat16 or float32 tensor")
+    shape, dv, dt = v.shape, v.device, v.dtype
+    b, d = shape
+    _out(state, "state", torch.float32, b * d, dv)
+    f = dict(batch=b, seqlen=1, dim=d, dtype=_DTYPE_IDS[dt], h_final=state)
+    with _on(dv):
+        if y is None:
+            y = torch.empty(shape, dtype=dt, device=dv)
+        for t, name in ((v, "v"), (g, "g"), (z, "z"), (y, "y")):
+            if t is not None:
+                _row_tensor(t, name, shape, dt, dv)
+                f[name] = t.data_ptr()
+                f[name + "_batch_stride"] = t.stride(0)
+        N.ssmq_gated_update(torch.cuda.current_stream().cuda_stream, **f)
+    return y

@@ -607,3 +607,243 @@ ssmq_status ssmq_selective_state_update_w8(const ssmq_m1_decode_args* a, void* s
 }
 
 }  // extern "C"
+
+// ---- strided-row operators -----------------------------------------------------
+namespace {
+
+int elem_size(int32_t dtype) { return dtype == SSMQ_F32 ? 4 : 2; }
+bool is_dtype(int32_t dtype) {
+  return dtype == SSMQ_F32 || dtype == SSMQ_F16 || dtype == SSMQ_BF16;
+}
+
+// A (batch, rows, width) tensor of contiguous rows, as bytes.
+struct Region {
+  uintptr_t lo = 0, hi = 0;  // [lo, hi); empty without a tensor
+  int64_t bs = 0, rs = 0, width = 0;  // strides and row length in bytes
+  bool any() const { return hi > lo; }
+};
+
+// Strides and alignment of a tensor's rows.  Outputs may not overlap themselves.
+ssmq_status check_rows(const void* p, int64_t b, int64_t L, int64_t d, int64_t bs, int64_t rs,
+                       int e, bool out, const char* name, const char* fn, Region* r) {
+  *r = Region();
+  if (!p) return SSMQ_OK;
+  REQUIRE(reinterpret_cast<uintptr_t>(p) % (uintptr_t)e == 0, SSMQ_ERR_ALIGNMENT,
+          "%s: %s is not on a %d-byte element", fn, name, e);
+  if (b == 0 || L == 0 || d == 0) return SSMQ_OK;
+  REQUIRE(L == 1 || rs >= d, SSMQ_ERR_INVALID_ARG, "%s: %s: row stride %lld below the row's %lld",
+          fn, name, (long long)rs, (long long)d);
+  REQUIRE(b == 1 || bs >= 0, SSMQ_ERR_INVALID_ARG, "%s: %s: negative batch stride", fn, name);
+  const __int128 rows = (L > 1 ? (__int128)(L - 1) * rs : 0) + d;
+  const __int128 all = (b > 1 ? (__int128)(b - 1) * bs : 0) + rows;
+  REQUIRE(all < ((__int128)1 << 59), SSMQ_ERR_INVALID_ARG, "%s: %s: size overflow", fn, name);
+  REQUIRE(!out || b == 1 || bs >= rows, SSMQ_ERR_INVALID_ARG,
+          "%s: %s: batch stride %lld makes sequences overlap", fn, name, (long long)bs);
+  r->lo = reinterpret_cast<uintptr_t>(p);
+  r->hi = r->lo + (uintptr_t)all * e;
+  r->bs = b > 1 ? bs * e : 0;
+  r->rs = L > 1 ? rs * e : 0;
+  r->width = d * e;
+  return SSMQ_OK;
+}
+Region dense(const void* p, int64_t bytes) {
+  Region r;
+  if (p && bytes > 0) {
+    r.lo = reinterpret_cast<uintptr_t>(p);
+    r.hi = r.lo + (uintptr_t)bytes;
+    r.width = bytes;
+  }
+  return r;
+}
+bool same(const Region& a, const Region& b) {
+  return a.lo == b.lo && a.hi == b.hi && a.bs == b.bs && a.rs == b.rs;
+}
+// Whether two tensors share a byte, as far as ranges and strides tell: column
+// slices of one tensor (equal strides, disjoint columns) do not.
+bool overlap(const Region& a, const Region& b) {
+  if (!a.any() || !b.any() || a.hi <= b.lo || b.hi <= a.lo) return false;
+  if (a.rs > 0 && a.rs == b.rs && a.bs == b.bs && a.bs % a.rs == 0) {
+    const int64_t off = (int64_t)((a.lo < b.lo ? b.lo - a.lo : a.lo - b.lo) % (uintptr_t)a.rs);
+    const int64_t first = a.lo < b.lo ? a.width : b.width;
+    const int64_t second = a.lo < b.lo ? b.width : a.width;
+    if (off >= first && off + second <= a.rs) return false;
+  }
+  return true;
+}
+struct Named {
+  const char* name;
+  Region r;
+};
+// Every output against the inputs and the other outputs; an output may be
+// exactly one of the inputs flagged in `may`.
+ssmq_status check_overlaps(const Named* in, const bool* may, int n_in, const Named* out, int n_out,
+                           const char* fn) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < n_in; ++j)
+      REQUIRE(!overlap(out[i].r, in[j].r) || (may[j] && same(out[i].r, in[j].r)),
+              SSMQ_ERR_INVALID_ARG, "%s: %s overlaps %s", fn, out[i].name, in[j].name);
+    for (int j = 0; j < i; ++j)
+      REQUIRE(!overlap(out[i].r, out[j].r), SSMQ_ERR_INVALID_ARG, "%s: %s overlaps %s", fn,
+              out[i].name, out[j].name);
+  }
+  return SSMQ_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+ssmq_status check_gated_sizes(int64_t b, int64_t L, int64_t d, int32_t dtype, const char* fn) {
+  REQUIRE(is_dtype(dtype), SSMQ_ERR_INVALID_ARG, "%s: bad dtype %d", fn, (int)dtype);
+  REQUIRE(b >= 0 && L >= 0 && d >= 0, SSMQ_ERR_INVALID_ARG, "%s: negative size", fn);
+  REQUIRE(b < ((int64_t)1 << 31) && d < ((int64_t)1 << 31) && L < ((int64_t)1 << 40) &&
+              b * ((d + 15) / 16) <= ((int64_t)1 << 27),
+          SSMQ_ERR_UNSUPPORTED, "%s: too many channels", fn);
+  return SSMQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ssmq_status ssmq_rms_norm_quantize(const ssmq_norm_args* a, void* stream) {
+  const char* fn = "ssmq_rms_norm_quantize";
+  Range nvtx_range(fn);
+  REQUIRE(a != nullptr, SSMQ_ERR_INVALID_ARG, "%s: args is NULL", fn);
+  REQUIRE(is_dtype(a->dtype), SSMQ_ERR_INVALID_ARG, "%s: bad dtype %d", fn, (int)a->dtype);
+  REQUIRE(a->tokens >= 0 && a->dim >= 1, SSMQ_ERR_INVALID_ARG,
+          "%s: need tokens >= 0 and dim >= 1", fn);
+  REQUIRE(a->dim <= 32768 && a->tokens <= 0x7fffffff, SSMQ_ERR_UNSUPPORTED,
+          "%s: dim > 32768 or tokens > 2^31 - 1", fn);
+  REQUIRE(a->eps >= 0.0f, SSMQ_ERR_INVALID_ARG, "%s: eps must be >= 0", fn);
+  REQUIRE((a->codes != nullptr) == (a->scales != nullptr), SSMQ_ERR_INVALID_ARG,
+          "%s: codes and scales come together", fn);
+  if (a->tokens == 0) return SSMQ_OK;
+  REQUIRE(a->x && (a->codes || a->y), SSMQ_ERR_INVALID_ARG, "%s: x, or every output, is NULL", fn);
+  REQUIRE(aligned4(a->weight) && aligned4(a->scales) && aligned4(a->status), SSMQ_ERR_ALIGNMENT,
+          "%s: weight, scales and status must be 4-byte aligned", fn);
+  const int e = elem_size(a->dtype);
+  Named in[3] = {{"x", {}}, {"residual", {}}, {"weight", dense(a->weight, 4 * a->dim)}};
+  Named out[4] = {{"residual_out", {}}, {"y", {}}, {"codes", {}},
+                  {"scales", dense(a->scales, 4 * a->tokens)}};
+  CHECK(check_rows(a->x, 1, a->tokens, a->dim, 0, a->x_stride, e, false, "x", fn, &in[0].r));
+  CHECK(check_rows(a->residual, 1, a->tokens, a->dim, 0, a->residual_stride, e, false, "residual",
+                   fn, &in[1].r));
+  CHECK(check_rows(a->residual_out, 1, a->tokens, a->dim, 0, a->residual_out_stride, e, true,
+                   "residual_out", fn, &out[0].r));
+  CHECK(check_rows(a->y, 1, a->tokens, a->dim, 0, a->y_stride, e, true, "y", fn, &out[1].r));
+  CHECK(check_rows(a->codes, 1, a->tokens, a->dim, 0, a->codes_stride, 1, true, "codes", fn,
+                   &out[2].r));
+  const bool in_place[3] = {true, true, false}, never[3] = {false, false, false};
+  CHECK(check_overlaps(in, in_place, 3, out, 1, fn));
+  CHECK(check_overlaps(in, never, 3, out + 1, 3, fn));
+  for (int i = 1; i < 4; ++i)
+    REQUIRE(!overlap(out[0].r, out[i].r), SSMQ_ERR_INVALID_ARG, "%s: residual_out overlaps %s", fn,
+            out[i].name);
+  if (injected(fn)) return fail(SSMQ_ERR_CUDA, "%s: injected launch failure", fn);
+  return finish(ssmq::launch_rms_norm_quantize(*a, (cudaStream_t)stream), fn);
+}
+
+int32_t ssmq_gated_scan_state_steps(void) { return ssmq::kGatedStateSteps; }
+
+ssmq_status ssmq_gated_scan(const ssmq_gated_args* a, void* stream) {
+  const char* fn = "ssmq_gated_scan";
+  Range nvtx_range(fn);
+  REQUIRE(a != nullptr, SSMQ_ERR_INVALID_ARG, "%s: args is NULL", fn);
+  const int64_t b = a->batch, L = a->seqlen, d = a->dim;
+  CHECK(check_gated_sizes(b, L, d, a->dtype, fn));
+  if (b == 0 || d == 0) return SSMQ_OK;
+  REQUIRE(L == 0 || (a->v.p && a->g.p && a->y.p), SSMQ_ERR_INVALID_ARG, "%s: v, g or y is NULL",
+          fn);
+  REQUIRE(aligned4(a->h0) && aligned4(a->h_final) && aligned4(a->states) && aligned4(a->lengths),
+          SSMQ_ERR_ALIGNMENT, "%s: h0, h_final, states and lengths must be 4-byte aligned", fn);
+  const int e = elem_size(a->dtype);
+  const int64_t saved = (L + ssmq::kGatedStateSteps - 1) / ssmq::kGatedStateSteps;
+  Named in[5] = {{"z", {}}, {"v", {}}, {"g", {}}, {"h0", dense(a->h0, 4 * b * d)},
+                 {"lengths", dense(a->lengths, 4 * b)}};
+  Named out[3] = {{"y", {}}, {"h_final", dense(a->h_final, 4 * b * d)},
+                  {"states", dense(a->states, 4 * b * saved * d)}};
+  const ssmq_rows* rows[4] = {&a->z, &a->v, &a->g, &a->y};
+  for (int i = 0; i < 4; ++i)
+    CHECK(check_rows(rows[i]->p, b, L, d, rows[i]->batch_stride, rows[i]->row_stride, e, i == 3,
+                     i < 3 ? in[i].name : "y", fn, i < 3 ? &in[i].r : &out[0].r));
+  const bool may_y[5] = {true, false, false, false, false};
+  const bool may_h[5] = {false, false, false, true, false}, never[5] = {};
+  CHECK(check_overlaps(in, may_y, 5, out, 1, fn));
+  CHECK(check_overlaps(in, may_h, 5, out + 1, 1, fn));
+  CHECK(check_overlaps(in, never, 5, out + 2, 1, fn));
+  REQUIRE(!overlap(out[1].r, out[2].r), SSMQ_ERR_INVALID_ARG, "%s: states overlaps h_final", fn);
+  for (int i = 1; i < 3; ++i)
+    REQUIRE(!overlap(out[0].r, out[i].r), SSMQ_ERR_INVALID_ARG, "%s: y overlaps %s", fn,
+            out[i].name);
+  if (injected(fn)) return fail(SSMQ_ERR_CUDA, "%s: injected launch failure", fn);
+  return finish(ssmq::launch_gated_scan(*a, (cudaStream_t)stream), fn);
+}
+
+ssmq_status ssmq_gated_scan_backward(const ssmq_gated_grad_args* a, void* stream) {
+  const char* fn = "ssmq_gated_scan_backward";
+  Range nvtx_range(fn);
+  REQUIRE(a != nullptr, SSMQ_ERR_INVALID_ARG, "%s: args is NULL", fn);
+  const int64_t b = a->batch, L = a->seqlen, d = a->dim;
+  CHECK(check_gated_sizes(b, L, d, a->dtype, fn));
+  if (b == 0 || d == 0) return SSMQ_OK;
+  REQUIRE(L == 0 || (a->v.p && a->g.p && a->dy.p && a->states && a->dv.p && a->dg.p),
+          SSMQ_ERR_INVALID_ARG, "%s: v, g, dy, states, dv or dg is NULL", fn);
+  REQUIRE(L == 0 || (a->z.p != nullptr) == (a->dz.p != nullptr), SSMQ_ERR_INVALID_ARG,
+          "%s: z and dz come together", fn);
+  REQUIRE(aligned4(a->states) && aligned4(a->dh_final) && aligned4(a->dh0) && aligned4(a->lengths),
+          SSMQ_ERR_ALIGNMENT, "%s: states, dh_final, dh0 and lengths must be 4-byte aligned", fn);
+  const int e = elem_size(a->dtype);
+  const int64_t saved = (L + ssmq::kGatedStateSteps - 1) / ssmq::kGatedStateSteps;
+  Named in[7] = {{"v", {}}, {"g", {}}, {"z", {}}, {"dy", {}},
+                 {"states", dense(a->states, 4 * b * saved * d)},
+                 {"dh_final", dense(a->dh_final, 4 * b * d)},
+                 {"lengths", dense(a->lengths, 4 * b)}};
+  Named out[4] = {{"dv", {}}, {"dg", {}}, {"dz", {}}, {"dh0", dense(a->dh0, 4 * b * d)}};
+  const ssmq_rows* rows[7] = {&a->v, &a->g, &a->z, &a->dy, &a->dv, &a->dg, &a->dz};
+  for (int i = 0; i < 7; ++i)
+    CHECK(check_rows(rows[i]->p, b, L, d, rows[i]->batch_stride, rows[i]->row_stride, e, i >= 4,
+                     i < 4 ? in[i].name : out[i - 4].name, fn, i < 4 ? &in[i].r : &out[i - 4].r));
+  const bool may[7] = {true, true, true, true, false, false, false};
+  const bool may_dh[7] = {false, false, false, false, false, true, false};
+  CHECK(check_overlaps(in, may, 7, out, 3, fn));
+  CHECK(check_overlaps(in, may_dh, 7, out + 3, 1, fn));
+  for (int i = 0; i < 3; ++i)
+    REQUIRE(!overlap(out[i].r, out[3].r), SSMQ_ERR_INVALID_ARG, "%s: dh0 overlaps %s", fn,
+            out[i].name);
+  if (injected(fn)) return fail(SSMQ_ERR_CUDA, "%s: injected launch failure", fn);
+  return finish(ssmq::launch_gated_scan_backward(*a, (cudaStream_t)stream), fn);
+}
+
+ssmq_status ssmq_gated_update(const ssmq_gated_args* a, void* stream) {
+  const char* fn = "ssmq_gated_update";
+  Range nvtx_range(fn);
+  REQUIRE(a != nullptr, SSMQ_ERR_INVALID_ARG, "%s: args is NULL", fn);
+  const int64_t b = a->batch, d = a->dim;
+  CHECK(check_gated_sizes(b, a->seqlen, d, a->dtype, fn));
+  REQUIRE(a->seqlen == 1, SSMQ_ERR_INVALID_ARG, "%s: seqlen must be 1", fn);
+  REQUIRE(!a->states && !a->lengths, SSMQ_ERR_INVALID_ARG,
+          "%s: states and lengths must be NULL", fn);
+  if (b == 0 || d == 0) return SSMQ_OK;
+  REQUIRE(a->v.p && a->g.p && a->y.p && a->h_final, SSMQ_ERR_INVALID_ARG,
+          "%s: v, g, y or the state (h_final) is NULL", fn);
+  REQUIRE(aligned4(a->h_final), SSMQ_ERR_ALIGNMENT, "%s: the state must be 4-byte aligned", fn);
+  const int e = elem_size(a->dtype);
+  Named in[3] = {{"z", {}}, {"v", {}}, {"g", {}}};
+  Named out[2] = {{"y", {}}, {"the state", dense(a->h_final, 4 * b * d)}};
+  const ssmq_rows* rows[4] = {&a->z, &a->v, &a->g, &a->y};
+  // (the sequences are the rows of one batch)
+  for (int i = 0; i < 4; ++i)
+    CHECK(check_rows(rows[i]->p, b, 1, d, rows[i]->batch_stride, d, e, i == 3,
+                     i < 3 ? in[i].name : "y", fn, i < 3 ? &in[i].r : &out[0].r));
+  for (Region* r : {&in[0].r, &in[1].r, &in[2].r, &out[0].r}) {
+    r->rs = r->bs;
+    r->bs = 0;
+  }
+  const bool may[3] = {true, false, false}, never[3] = {false, false, false};
+  CHECK(check_overlaps(in, may, 3, out, 1, fn));
+  CHECK(check_overlaps(in, never, 3, out + 1, 1, fn));
+  REQUIRE(!overlap(out[0].r, out[1].r), SSMQ_ERR_INVALID_ARG, "%s: y overlaps the state", fn);
+  if (injected(fn)) return fail(SSMQ_ERR_CUDA, "%s: injected launch failure", fn);
+  return finish(ssmq::launch_gated_update(*a, (cudaStream_t)stream), fn);
+}
+
+}  // extern "C"

@@ -1,0 +1,221 @@
+// Gradient of the gated linear recurrence (sm_100a).
+//
+// With f = sigmoid(g), n = 1 - f, h_t = f_t h_{t-1} + n_t v_t, y_t = h_t silu(z_t)
+// and l_t the gradient that reaches h_t,
+//   l_t = dy_t silu(z_t) + c_{t+1},  c_t = f_t l_t  (c behind the last step: dh_final)
+//   dv_t = n_t l_t,  dg_t = f_t n_t (h_{t-1} - v_t) l_t,  dz_t = dy_t h_t silu'(z_t).
+// c is a second recurrence, run backwards with the same decays: a segment maps
+// the c behind it to the c in front of it as c -> A c + R with the A of its
+// forward map.
+//
+// Bound: HBM (v, g, z, dy in, dv, dg, dz out).  A tile's steps stay in
+// registers: the forward states inside it are rebuilt from the state that the
+// forward call saved at its start (one per 64 steps), so neither h nor the
+// gates cross memory, and only c travels between the CTAs of a cluster.
+#include "gated.cuh"
+
+namespace ssmq {
+namespace {
+
+using namespace gated;
+
+struct GradParams {
+  int64_t L, d, blocks;
+  int64_t tiles, saved;
+  Rows v, g, z, dy, dv, dg, dz;
+  const float* states;
+  const float* dh_final;
+  float* dh0;
+  const int32_t* lengths;
+};
+
+template <typename T, bool kVec, int kLanes, bool kGate>
+__global__ void __launch_bounds__(kThreads, 2) gated_scan_grad_kernel(const GradParams p) {
+  __shared__ Shared<kLanes> sh;
+  __shared__ float4 s_fwd[2][kWarps][kLanes];
+  using TileT = Tile<kLanes>;
+  const uint32_t size = cluster_size(), rank = cluster_rank();
+  const int64_t unit = blockIdx.x / size;
+  const int64_t seq = unit / p.blocks, blk = unit % p.blocks;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = lane / kLanes, l = lane % kLanes;
+  const int64_t c0 = blk * TileT::kChannels + (kVec ? 2 * l : l);
+  constexpr int kNext = kVec ? 1 : kLanes;
+  const bool in0 = c0 < p.d, in1 = c0 + kNext < p.d;
+  int64_t end = p.L;
+  if (p.lengths) {
+    const int64_t n = p.lengths[seq];
+    end = n < 0 ? 0 : (n < p.L ? n : p.L);
+  }
+  const T* vp = static_cast<const T*>(p.v.p) + seq * p.v.bs + c0;
+  const T* gp = static_cast<const T*>(p.g.p) + seq * p.g.bs + c0;
+  const T* zp = kGate ? static_cast<const T*>(p.z.p) + seq * p.z.bs + c0 : nullptr;
+  const T* dyp = static_cast<const T*>(p.dy.p) + seq * p.dy.bs + c0;
+  T* dvp = static_cast<T*>(p.dv.p) + seq * p.dv.bs + c0;
+  T* dgp = static_cast<T*>(p.dg.p) + seq * p.dg.bs + c0;
+  T* dzp = kGate ? static_cast<T*>(p.dz.p) + seq * p.dz.bs + c0 : nullptr;
+  const int first = (warp * TileT::kSubs + sub) * kSteps;
+
+  float2 c = make_float2(0.0f, 0.0f);
+  if (p.dh_final) {
+    if (in0) c.x = p.dh_final[seq * p.d + c0];
+    if (in1) c.y = p.dh_final[seq * p.d + c0 + kNext];
+  }
+
+  const int64_t rounds = (p.tiles + size - 1) / size;
+  for (int64_t k = 0; k < rounds; ++k) {
+    // tiles from the last one backwards; rank 0 holds the latest of a round
+    const int64_t tile = p.tiles - 1 - (k * size + rank);
+    const int64_t t0 = tile * TileT::kLen + first;
+    const bool real = tile >= 0;
+    Pair<T> rv[kSteps], rg[kSteps], rz[kSteps], rd[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const bool on = real && t0 + i < end;
+      const int64_t t = t0 + i;
+      rg[i] = load_pair<T, kVec, kLanes>(gp + t * p.g.rs, on && in0, on && in1);
+      rv[i] = load_pair<T, kVec, kLanes>(vp + t * p.v.rs, on && in0, on && in1);
+      rd[i] = load_pair<T, kVec, kLanes>(dyp + t * p.dy.rs, on && in0, on && in1);
+      if constexpr (kGate)
+        rz[i] = load_pair<T, kVec, kLanes>(zp + t * p.z.rs, on && in0, on && in1);
+    }
+    float2 hs = make_float2(0.0f, 0.0f);  // state before the tile
+    if (real) {
+      const float* sp = p.states +
+                        (seq * p.saved + tile * (TileT::kLen / kGatedStateSteps)) * p.d + c0;
+      if (in0) hs.x = sp[0];
+      if (in1) hs.y = sp[kNext];
+    }
+
+    float2 f[kSteps], n[kSteps], dh[kSteps];
+    float2 a = make_float2(1.0f, 1.0f), b = make_float2(0.0f, 0.0f), r = b;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const float2 g = pair_f32<T>(rg[i]);
+      gate_pair(g.x, f[i].x, n[i].x);
+      gate_pair(g.y, f[i].y, n[i].y);
+      if (!real || t0 + i >= end) {
+        f[i] = make_float2(1.0f, 1.0f);
+        n[i] = make_float2(0.0f, 0.0f);
+      }
+      a = fmul2(a, f[i]);
+      b = ffma2(f[i], b, fmul2(n[i], pair_f32<T>(rv[i])));
+      dh[i] = pair_f32<T>(rd[i]);
+      if constexpr (kGate) {
+        const float2 z = pair_f32<T>(rz[i]);
+        dh[i] = fmul2(dh[i], make_float2(z.x * sigmoid_sfu(z.x), z.y * sigmoid_sfu(z.y)));
+      }
+    }
+#pragma unroll
+    for (int i = kSteps - 1; i >= 0; --i) r = fmul2(f[i], fadd2(dh[i], r));
+
+    // forward state before this thread's segment: maps of the CTA's earlier segments
+    const int buf = (int)(k & 1);
+    {
+      float4 m = make_float4(a.x, a.y, b.x, b.y);
+      constexpr int kSubs = TileT::kSubs;
+#pragma unroll
+      for (int o = 1; o < kSubs; o <<= 1) {
+        const float4 before = shfl_f4(m, (lane - o * kLanes) & 31);
+        if (sub >= o) m = compose(before, m);
+      }
+      if (sub == kSubs - 1) s_fwd[buf][warp][l] = m;
+      float4 mine = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+      if constexpr (kSubs > 1) {
+        const float4 before = shfl_f4(m, (lane - kLanes) & 31);
+        if (sub > 0) mine = before;
+      }
+      // (the barrier inside carry_in orders s_fwd as well)
+      const float2 cin = carry_in<kLanes, true>(sh, buf, make_float4(a.x, a.y, r.x, r.y), c, rank,
+                                                size);
+      for (int w = 0; w < warp; ++w) hs = apply(s_fwd[buf][w][l], hs);
+      hs = apply(mine, hs);
+      r = cin;
+    }
+
+    float2 hb[kSteps];  // h_{t-1}
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      hb[i] = hs;
+      hs = ffma2(f[i], hs, fmul2(n[i], pair_f32<T>(rv[i])));
+    }
+    if (real) {
+#pragma unroll
+      for (int i = kSteps - 1; i >= 0; --i) {
+        const int64_t t = t0 + i;
+        const bool on = t < p.L;
+        const float2 lam = fadd2(dh[i], r);
+        float2 dv = fmul2(n[i], lam);
+        r = fmul2(f[i], lam);
+        float2 dg = fmul2(dv, fmul2(f[i], fsub2(hb[i], pair_f32<T>(rv[i]))));
+        if (t >= end) dv = dg = make_float2(0.0f, 0.0f);
+        store_pair<T, kVec, kLanes>(dvp + t * p.dv.rs, dv, on && in0, on && in1);
+        store_pair<T, kVec, kLanes>(dgp + t * p.dg.rs, dg, on && in0, on && in1);
+        if constexpr (kGate) {
+          const float2 z = pair_f32<T>(rz[i]);
+          const float2 d = pair_f32<T>(rd[i]);
+          const float2 h = i + 1 < kSteps ? hb[i + 1 < kSteps ? i + 1 : i] : hs;
+          const float sx = sigmoid_sfu(z.x), sy = sigmoid_sfu(z.y);
+          float2 dz = make_float2(d.x * h.x * (sx * fmaf(z.x, 1.0f - sx, 1.0f)),
+                                  d.y * h.y * (sy * fmaf(z.y, 1.0f - sy, 1.0f)));
+          if (t >= end) dz = make_float2(0.0f, 0.0f);
+          store_pair<T, kVec, kLanes>(dzp + t * p.dz.rs, dz, on && in0, on && in1);
+        }
+      }
+    }
+  }
+  if (p.dh0 && rank == 0 && warp == 0 && sub == 0) {
+    float* o = p.dh0 + seq * p.d + c0;
+    if (in0) o[0] = c.x;
+    if (in1) o[kNext] = c.y;
+  }
+}
+
+template <typename T>
+cudaError_t grad_type(const ssmq_gated_grad_args& a, cudaStream_t st) {
+  const Shape s = shape_for(a.batch, a.seqlen, a.dim);
+  const int len = s.narrow ? Tile<8>::kLen : Tile<32>::kLen;
+  GradParams p;
+  p.L = a.seqlen;
+  p.d = a.dim;
+  p.blocks = s.blocks;
+  p.tiles = (a.seqlen + len - 1) / len;
+  p.saved = (a.seqlen + kGatedStateSteps - 1) / kGatedStateSteps;
+  p.v = rows_of(a.v);
+  p.g = rows_of(a.g);
+  p.z = rows_of(a.z);
+  p.dy = rows_of(a.dy);
+  p.dv = rows_of(a.dv);
+  p.dg = rows_of(a.dg);
+  p.dz = rows_of(a.dz);
+  p.states = a.states;
+  p.dh_final = a.dh_final;
+  p.dh0 = a.dh0;
+  p.lengths = a.lengths;
+  const bool z = a.z.p != nullptr;
+  const bool vec = a.dim % 2 == 0 && pairs_ok<T>(a.v) && pairs_ok<T>(a.g) && pairs_ok<T>(a.dy) &&
+                   pairs_ok<T>(a.dv) && pairs_ok<T>(a.dg) &&
+                   (!z || (pairs_ok<T>(a.z) && pairs_ok<T>(a.dz)));
+#define SSMQ_GATED(V, N, Z) return launch(gated_scan_grad_kernel<T, V, N, Z>, p, s, st)
+  if (vec) {
+    if (s.narrow) { if (z) SSMQ_GATED(true, 8, true); SSMQ_GATED(true, 8, false); }
+    if (z) SSMQ_GATED(true, 32, true);
+    SSMQ_GATED(true, 32, false);
+  }
+  if (s.narrow) { if (z) SSMQ_GATED(false, 8, true); SSMQ_GATED(false, 8, false); }
+  if (z) SSMQ_GATED(false, 32, true);
+  SSMQ_GATED(false, 32, false);
+#undef SSMQ_GATED
+}
+
+}  // namespace
+
+cudaError_t launch_gated_scan_backward(const ssmq_gated_grad_args& a, cudaStream_t st) {
+  switch (a.dtype) {
+    case SSMQ_F16: return grad_type<__half>(a, st);
+    case SSMQ_BF16: return grad_type<__nv_bfloat16>(a, st);
+    default: return grad_type<float>(a, st);
+  }
+}
+
+}  // namespace ssmq

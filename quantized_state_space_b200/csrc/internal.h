@@ -57,6 +57,14 @@ cudaError_t launch_percentile_abs(const void* src, bool f16, int64_t n, const do
                                   float* out, float* thr, float alpha, void* workspace,
                                   cudaStream_t st);
 
+cudaError_t launch_rms_norm_quantize(const ssmq_norm_args& a, cudaStream_t st);
+
+// Gated recurrence: steps between two saved states.
+constexpr int kGatedStateSteps = 64;
+cudaError_t launch_gated_scan(const ssmq_gated_args& a, cudaStream_t st);
+cudaError_t launch_gated_scan_backward(const ssmq_gated_grad_args& a, cudaStream_t st);
+cudaError_t launch_gated_update(const ssmq_gated_args& a, cudaStream_t st);
+
 // diagnostics: base-2 exponentials on the special-function unit
 cudaError_t launch_probe_ex2(int iters, float* sink, int64_t* n_ex2, cudaStream_t st);
 
