@@ -731,6 +731,49 @@ typedef struct {
 
 ssmq_status ssmq_rms_norm_quantize(const ssmq_norm_args* args, void* stream);
 
+/*
+ * ssmq_int8_linear: y[t][n] = fl(acc * fl32(x_scale[t] w_scale[n]) + bias[n]),
+ * acc = sum_k x[t][k] w[n][k] summed exactly in 32-bit integers, rounded once
+ * to dtype (the products and the bias in binary32).
+ *
+ * x            int8 (tokens, in_features), x_stride bytes apart: the codes of
+ *              ssmq_rms_norm_quantize, x_scale fp32[tokens] its scales
+ * w            int8 (out_features, in_features), w_stride bytes apart: the
+ *              codes of ssmq_quantize_groups with one group per row, w_scale
+ *              fp32[out_features]
+ * bias         fp32[out_features] or NULL
+ * y            (tokens, out_features) of dtype, y_stride elements apart;
+ *              overlaps no input
+ * workspace    device memory of ssmq_int8_linear_workspace_size(args) bytes,
+ *              256-byte aligned, contents need not be initialised: 0 bytes
+ *              when x and w start on 16-byte boundaries and their strides are
+ *              multiples of 16 (any in_features), else room for a copy on
+ *              such rows.  One call at a time per workspace.
+ * in_features == 0 gives the bias.  Supported: in_features <= 131071 (the
+ * sums stay inside 32 bits for every code, -128 among them).
+ * status: SSMQ_DEV_TIMEOUT if a bounded device wait gave up.
+ * Errors: INVALID_ARG (NULL, sizes, strides, overlaps, workspace), UNSUPPORTED
+ * (in_features, more than 2^31 - 1 tokens or channels), ALIGNMENT.
+ */
+typedef struct {
+  int64_t tokens, out_features, in_features;
+  int32_t dtype;            /* ssmq_dtype of y */
+  const int8_t* x;
+  int64_t x_stride;
+  const float* x_scale;
+  const int8_t* w;
+  int64_t w_stride;
+  const float* w_scale;
+  const float* bias;
+  void* y;
+  int64_t y_stride;
+  uint32_t* status;
+} ssmq_linear_args;
+
+size_t ssmq_int8_linear_workspace_size(const ssmq_linear_args* args);
+ssmq_status ssmq_int8_linear(const ssmq_linear_args* args, void* workspace, size_t ws_bytes,
+                             void* stream);
+
 /* ------------------------------------------------------------------------ */
 /* Gated linear recurrence                                                    */
 /* ------------------------------------------------------------------------ */

@@ -90,6 +90,13 @@ class NormArgs(C.Structure):
                 ("scales", _vp), ("status", _vp)]
 
 
+class LinearArgs(C.Structure):
+    _fields_ = [("tokens", _i64), ("out_features", _i64), ("in_features", _i64),
+                ("dtype", _i32), ("x", _vp), ("x_stride", _i64), ("x_scale", _vp), ("w", _vp),
+                ("w_stride", _i64), ("w_scale", _vp), ("bias", _vp), ("y", _vp),
+                ("y_stride", _i64), ("status", _vp)]
+
+
 def _rows(name):
     """The fields of one ssmq_rows member (pointer and strides), flattened."""
     return [(name, _vp), (name + "_batch_stride", _i64), (name + "_row_stride", _i64)]
@@ -143,6 +150,8 @@ SIGNATURES = {
     "ssmq_softedge_calibrate_noalloc": (_i32, [_vp, _i32, _i64, C.c_double, C.c_double, _f32,
                                                _vp, _vp]),
     "ssmq_rms_norm_quantize": (_i32, [C.POINTER(NormArgs), _vp]),
+    "ssmq_int8_linear_workspace_size": (C.c_size_t, [C.POINTER(LinearArgs)]),
+    "ssmq_int8_linear": (_i32, [C.POINTER(LinearArgs), _vp, C.c_size_t, _vp]),
     "ssmq_gated_scan_state_steps": (_i32, []),
     "ssmq_gated_scan": (_i32, [C.POINTER(GatedArgs), _vp]),
     "ssmq_gated_scan_backward": (_i32, [C.POINTER(GatedGradArgs), _vp]),
@@ -324,6 +333,16 @@ def ssmq_rms_norm_quantize(stream=None, **fields):
     """Fields of ssmq_norm_args as keywords (tensors for pointer fields)."""
     a = _struct(NormArgs, fields)
     _check(lib().ssmq_rms_norm_quantize(C.byref(a), _stream(stream)))
+
+
+def ssmq_int8_linear_workspace_size(**fields):
+    return int(lib().ssmq_int8_linear_workspace_size(C.byref(_struct(LinearArgs, fields))))
+
+
+def ssmq_int8_linear(workspace=None, ws_bytes=0, stream=None, **fields):
+    """Fields of ssmq_linear_args as keywords (tensors for pointer fields)."""
+    a = _struct(LinearArgs, fields)
+    _check(lib().ssmq_int8_linear(C.byref(a), ptr(workspace), ws_bytes, _stream(stream)))
 
 
 def ssmq_gated_scan_state_steps():

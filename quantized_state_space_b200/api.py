@@ -710,6 +710,55 @@ def rms_norm_quantize(x, weight=None, *, residual=None, eps=1e-5, residual_out=N
     return (codes, scales) + out
 
 
+def int8_linear(x, x_scale, w, w_scale, *, bias=None, out=None, dtype=None, workspace=None,
+                status=None):
+    """x @ w^T of int8 codes: x (..., K) with x_scale (...) float32 (one per
+    token), w (N, K) with w_scale (N,) float32 (one per output channel), bias
+    (N,) float32 or None; the sums are exact.  Returns (..., N) in ``dtype``
+    (float16 by default, bfloat16 or float32) or in out's.  Rows of x and w on
+    16-byte boundaries (such as the codes of rms_norm_quantize) are read in
+    place; others are first copied into ``workspace`` (uint8 bytes on the
+    device, allocated when not given)."""
+    dv, K = x.device, x.shape[-1]
+    if out is not None:
+        if dtype is not None and dtype != out.dtype:
+            raise ValueError("dtype %s differs from out's %s" % (dtype, out.dtype))
+        dtype = out.dtype
+    elif dtype is None:
+        dtype = torch.float16
+    if dtype not in _DTYPE_IDS:
+        raise ValueError("the output must be float16, bfloat16 or float32 (got %s)" % dtype)
+    xp, xst = _flat_rows(x, "x", x.shape, torch.int8, dv)
+    if w.dim() != 2:
+        raise ValueError("w must be (out_features, in_features)")
+    n = w.shape[0]
+    wp, wst = _flat_rows(w, "w", (n, K), torch.int8, dv)
+    lead = x.shape[:-1]
+    tokens = 1
+    for v in lead:
+        tokens *= v
+    _in(x_scale, "x_scale", torch.float32, tokens, dv)
+    _in(w_scale, "w_scale", torch.float32, n, dv)
+    _in(bias, "bias", torch.float32, n, dv)
+    _status(status, dv)
+    with _on(dv):
+        if out is None:
+            out = torch.empty((*lead, n), dtype=dtype, device=dv)
+        yp, yst = _flat_rows(out, "out", (*lead, n), dtype, dv)
+        f = dict(tokens=tokens, out_features=n, in_features=K, dtype=_DTYPE_IDS[dtype], x=xp,
+                 x_stride=xst, x_scale=x_scale, w=wp, w_stride=wst, w_scale=w_scale, bias=bias,
+                 y=yp, y_stride=yst, status=status)
+        ws, wptr = 0, None
+        if (xp | wp | xst | wst) % 16:
+            ws = N.ssmq_int8_linear_workspace_size(**f)
+            _workspace(workspace, ws, dv)
+            if ws and workspace is None:
+                workspace = torch.empty(ws + 256, dtype=torch.uint8, device=dv)
+            wptr = (workspace.data_ptr() + 255) // 256 * 256 if ws else None
+        N.ssmq_int8_linear(wptr, ws, torch.cuda.current_stream().cuda_stream, **f)
+    return out
+
+
 # ---- gated linear recurrence ----------------------------------------------------
 
 def _gated_rows(f, t, name, shape, dtype, device):

@@ -742,6 +742,53 @@ ssmq_status ssmq_rms_norm_quantize(const ssmq_norm_args* a, void* stream) {
   return finish(ssmq::launch_rms_norm_quantize(*a, (cudaStream_t)stream), fn);
 }
 
+size_t ssmq_int8_linear_workspace_size(const ssmq_linear_args* a) {
+  return a ? ssmq::int8_linear_workspace_bytes(*a) : 0;
+}
+
+ssmq_status ssmq_int8_linear(const ssmq_linear_args* a, void* workspace, size_t ws_bytes,
+                             void* stream) {
+  const char* fn = "ssmq_int8_linear";
+  Range nvtx_range(fn);
+  REQUIRE(a != nullptr, SSMQ_ERR_INVALID_ARG, "%s: args is NULL", fn);
+  REQUIRE(is_dtype(a->dtype), SSMQ_ERR_INVALID_ARG, "%s: bad dtype %d", fn, (int)a->dtype);
+  const int64_t M = a->tokens, N = a->out_features, K = a->in_features;
+  REQUIRE(M >= 0 && N >= 0 && K >= 0, SSMQ_ERR_INVALID_ARG, "%s: negative size", fn);
+  REQUIRE(K <= 131071, SSMQ_ERR_UNSUPPORTED,
+          "%s: in_features > 131071 (32-bit sums could overflow)", fn);
+  REQUIRE(M <= 0x7fffffff && N <= 0x7fffffff, SSMQ_ERR_UNSUPPORTED,
+          "%s: more than 2^31 - 1 tokens or channels", fn);
+  if (M == 0 || N == 0) return SSMQ_OK;
+  REQUIRE(a->x_scale && a->w_scale && a->y && (K == 0 || (a->x && a->w)), SSMQ_ERR_INVALID_ARG,
+          "%s: a required tensor is NULL", fn);
+  REQUIRE(aligned4(a->x_scale) && aligned4(a->w_scale) && aligned4(a->bias) &&
+              aligned4(a->status),
+          SSMQ_ERR_ALIGNMENT, "%s: scales, bias and status must be 4-byte aligned", fn);
+  Named in[5] = {{"x", {}}, {"w", {}}, {"x_scale", dense(a->x_scale, 4 * M)},
+                 {"w_scale", dense(a->w_scale, 4 * N)}, {"bias", dense(a->bias, 4 * N)}};
+  Named out[1] = {{"y", {}}};
+  CHECK(check_rows(a->x, 1, M, K, 0, a->x_stride, 1, false, "x", fn, &in[0].r));
+  CHECK(check_rows(a->w, 1, N, K, 0, a->w_stride, 1, false, "w", fn, &in[1].r));
+  CHECK(check_rows(a->y, 1, M, N, 0, a->y_stride, elem_size(a->dtype), true, "y", fn, &out[0].r));
+  REQUIRE(a->x_stride < ((int64_t)1 << 40) && a->w_stride < ((int64_t)1 << 40),
+          SSMQ_ERR_UNSUPPORTED, "%s: row stride of 2^40 bytes or more", fn);
+  const bool never[5] = {};
+  CHECK(check_overlaps(in, never, 5, out, 1, fn));
+  const size_t need = ssmq::int8_linear_workspace_bytes(*a);
+  if (need) {
+    REQUIRE(workspace && ws_bytes >= need, SSMQ_ERR_INVALID_ARG,
+            "%s: workspace of %zu bytes required (got %zu)", fn, need, ws_bytes);
+    REQUIRE((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0, SSMQ_ERR_ALIGNMENT,
+            "%s: workspace must be 256-byte aligned", fn);
+    const Named room[1] = {{"the workspace", dense(workspace, (int64_t)need)}};
+    CHECK(check_overlaps(in, never, 5, room, 1, fn));
+    REQUIRE(!overlap(room[0].r, out[0].r), SSMQ_ERR_INVALID_ARG, "%s: y overlaps the workspace",
+            fn);
+  }
+  if (injected(fn)) return fail(SSMQ_ERR_CUDA, "%s: injected launch failure", fn);
+  return finish(ssmq::launch_int8_linear(*a, workspace, (cudaStream_t)stream), fn);
+}
+
 int32_t ssmq_gated_scan_state_steps(void) { return ssmq::kGatedStateSteps; }
 
 ssmq_status ssmq_gated_scan(const ssmq_gated_args* a, void* stream) {

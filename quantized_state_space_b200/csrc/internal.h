@@ -59,6 +59,9 @@ cudaError_t launch_percentile_abs(const void* src, bool f16, int64_t n, const do
 
 cudaError_t launch_rms_norm_quantize(const ssmq_norm_args& a, cudaStream_t st);
 
+size_t int8_linear_workspace_bytes(const ssmq_linear_args& a);
+cudaError_t launch_int8_linear(const ssmq_linear_args& a, void* ws, cudaStream_t st);
+
 // Gated recurrence: steps between two saved states.
 constexpr int kGatedStateSteps = 64;
 cudaError_t launch_gated_scan(const ssmq_gated_args& a, cudaStream_t st);

@@ -1,0 +1,684 @@
+// W8A8 matrix product with one scale per token and one per output channel
+// (sm_100a tensor cores).
+//
+// Quamba2 (shd-paper.top card), abstract: W8A8, 8-bit weights times 8-bit
+// activations.  y[t][n] = round(acc (x_scale[t] w_scale[n]) + bias[n]) with
+// acc = sum_k x[t][k] w[n][k] in 32-bit integers (tcgen05.mma kind::i8), so
+// the sum is exact and its order does not matter.
+//
+// Orientation: the weights are the MMA's A operand (its M rows are output
+// channels) and the tokens its B operand (its N columns), at every size.  An
+// accumulator lane is then a channel and a column a token, so N follows the
+// token count down to 16 without idle MMA rows, and the 32 lanes of a warp
+// store 32 consecutive channels of one token: whole sectors straight from
+// registers, at any alignment.
+//
+// Both operands are K-major, brought in by TMA as 128-byte rows in the
+// 128-byte swizzle (32 bytes, one MMA K-step, per quarter row); rows and
+// columns beyond the tensor read as zero.
+#include <cuda.h>
+
+#include "internal.h"
+#include "stream.cuh"
+#include "tc.cuh"
+#include "vec8.cuh"
+
+namespace ssmq {
+namespace {
+
+constexpr int kBlockK = 128;                 // bytes of K per stage
+constexpr int kRows = 128;                   // operand rows of one TMA box (weights)
+constexpr int kOperand = kRows * kBlockK;    // 16 KB
+constexpr uint32_t kWaitLimit = 1u << 20;
+
+struct LinParams {
+  int64_t M, N;      // tokens, channels
+  int kblocks;
+  const float* xs;
+  const float* ws;
+  const float* bias;
+  void* y;
+  int64_t ldy;
+  int dtype;
+  uint32_t* status;
+  int64_t tok_tiles, ch_tiles, group;  // persistent kernel: tile order
+};
+
+// ---- PTX ---------------------------------------------------------------------
+__device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int k, int row,
+                                         uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(k), "r"(row), "r"(bar)
+      : "memory");
+}
+// the same for a CTA pair: bar may lie in either CTA of the pair
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int k, int row,
+                                              uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(k), "r"(row), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+// K-major operand in the 128-byte swizzle: 8-row groups 1024 bytes apart
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
+  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)1u << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+// kind::i8: signed A and B, 32-bit integer accumulator
+__host__ __device__ constexpr uint32_t idesc_i8(int M, int N) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+template <int kGroup>
+__device__ __forceinline__ void mma_i8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  if constexpr (kGroup == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+// arrive on `bar` of both CTAs of the pair once this thread's MMAs are done
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(tc::smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+// 16 columns of this thread's TMEM lane, complete when the statement ends
+__device__ __forceinline__ void tmem_ld16i(uint32_t taddr, int (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// ---- epilogue: one lane's channel, consecutive tokens --------------------------
+struct Channel {
+  int64_t n;
+  bool in;
+  float scale, bias;
+};
+__device__ __forceinline__ Channel channel_of(const LinParams& p, int64_t n) {
+  Channel c;
+  c.n = n;
+  c.in = n < p.N;
+  c.scale = c.in ? __ldg(p.ws + n) : 0.0f;
+  c.bias = c.in && p.bias ? __ldg(p.bias + n) : 0.0f;
+  return c;
+}
+template <typename T>
+__device__ __forceinline__ void store_one(const LinParams& p, const Channel& c, int64_t t, int acc) {
+  if (t < p.M && c.in) {
+    const float v = fmaf((float)acc, __ldg(p.xs + t) * c.scale, c.bias);
+    static_cast<T*>(p.y)[t * p.ldy + c.n] = from_f32<T>(v);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store16(const LinParams& p, const Channel& c, int64_t t0,
+                                        const int (&acc)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) store_one<T>(p, c, t0 + i, acc[i]);
+}
+__device__ __forceinline__ void store16_any(const LinParams& p, const Channel& c, int64_t t0,
+                                            const int (&acc)[16]) {
+  if (p.dtype == SSMQ_F16)
+    store16<__half>(p, c, t0, acc);
+  else if (p.dtype == SSMQ_BF16)
+    store16<__nv_bfloat16>(p, c, t0, acc);
+  else
+    store16<float>(p, c, t0, acc);
+}
+
+// ---- few tokens: 128 channels x kTok tokens per cluster, K split over its CTAs --
+// Bound: the weight bytes (HBM).  The channel tiles alone are too few to pull
+// the memory's bandwidth, so the CTAs of a cluster take consecutive parts of K
+// of the same tile; each CTA then sums its share of the token columns from all
+// parts (32-bit integers pushed through distributed shared memory: exact, no
+// workspace, no second launch).
+constexpr int kSplitThreads = 192;  // 4 epilogue warps, 1 TMA, 1 MMA
+constexpr int kMaxSplit = 8;
+
+template <int kTok>
+struct SplitCfg {
+  static constexpr int kStage = kOperand + kTok * kBlockK;
+  static constexpr int kRed = kTok <= 128 ? kTok * kRows * 4 : 0;
+  // two CTAs per SM up to 64 tokens, so that a cluster finds its SMs easily
+  static constexpr int kBudget = (kTok <= 64 ? 108 : 216) * 1024;
+  static constexpr int kStages = (kBudget - kRed) / kStage;
+  static constexpr int kSmem = 1024 + kStages * kStage + kRed + 256;
+  static constexpr int kCols = kTok < 32 ? 32 : kTok;
+};
+
+template <int kTok>
+__global__ void __launch_bounds__(kSplitThreads)
+    int8_linear_split_kernel(const __grid_constant__ CUtensorMap wmap,
+                             const __grid_constant__ CUtensorMap xmap, const LinParams p,
+                             const int split) {
+  using Cfg = SplitCfg<kTok>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~1023ull);
+  int* red = reinterpret_cast<int*>(base + Cfg::kStages * Cfg::kStage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(base + Cfg::kStages * Cfg::kStage + Cfg::kRed);
+  uint64_t* empty = full + Cfg::kStages;
+  uint64_t* done = empty + Cfg::kStages;
+  uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile uint32_t* gave_up = slot + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = split > 1 ? cta_rank() : 0;
+  const int64_t tile = blockIdx.x / split;
+  const int64_t ch0 = (tile % p.ch_tiles) * kRows, tok0 = (tile / p.ch_tiles) * kTok;
+  const int kb0 = (int)((int64_t)p.kblocks * rank / split);
+  const int kb1 = (int)((int64_t)p.kblocks * (rank + 1) / split);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Cfg::kStages; ++i) {
+      tc::mbar_init(full + i, 1);
+      tc::mbar_init(empty + i, 1);
+    }
+    tc::mbar_init(done, 1);
+    *gave_up = 0;
+  }
+  if (warp == 5) tc::tmem_alloc(slot, Cfg::kCols);
+  tc::fence_before();
+  __syncthreads();
+  if (split > 1) cluster_sync();  // every CTA of the cluster runs before one pushes to it
+  tc::fence_after();
+  const uint32_t tmem = *slot;
+
+  if (warp == 4 && lane == 0) {
+    prefetch_map(&wmap);
+    prefetch_map(&xmap);
+    int i = 0;
+    for (int kb = kb0; kb < kb1; ++kb, ++i) {
+      const int s = i % Cfg::kStages;
+      if (i >= Cfg::kStages &&
+          !tc::mbar_wait(empty + s, (uint32_t)(i / Cfg::kStages - 1) & 1u, kWaitLimit)) {
+        *gave_up = 1;
+        break;
+      }
+      const uint32_t bar = tc::smem_u32(full + s);
+      const uint32_t dst = tc::smem_u32(base + s * Cfg::kStage);
+      stream::expect_tx(full + s, Cfg::kStage);
+      tma_load(dst, &wmap, kb * kBlockK, (int)ch0, bar);
+      tma_load(dst + kOperand, &xmap, kb * kBlockK, (int)tok0, bar);
+    }
+    if (*gave_up) {  // copies in flight land before the CTA leaves
+      for (int j = i > Cfg::kStages ? i - Cfg::kStages : 0; j < i; ++j)
+        tc::mbar_wait(full + j % Cfg::kStages, (uint32_t)(j / Cfg::kStages) & 1u, kWaitLimit);
+    }
+  } else if (warp == 5 && lane == 0) {
+    constexpr uint32_t idesc = idesc_i8(kRows, kTok);
+    int i = 0;
+    for (int kb = kb0; kb < kb1; ++kb, ++i) {
+      const int s = i % Cfg::kStages;
+      if (!tc::mbar_wait(full + s, (uint32_t)(i / Cfg::kStages) & 1u, kWaitLimit)) {
+        *gave_up = 1;
+        break;
+      }
+      tc::fence_after();
+      const uint32_t a = tc::smem_u32(base + s * Cfg::kStage);
+      const uint64_t ad = sw128_desc(a), bd = sw128_desc(a + kOperand);
+#pragma unroll
+      for (int q = 0; q < kBlockK / 32; ++q)
+        mma_i8<1>(tmem, ad + 2 * q, bd + 2 * q, idesc, i > 0 || q > 0);
+      tc::mma_commit(empty + s);
+    }
+    tc::mma_commit(done);
+  }
+  __syncwarp();
+
+  const Channel c = channel_of(p, ch0 + (warp & 3) * 32 + lane);
+  const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+  if (warp < 4) {
+    if (!tc::mbar_wait(done, 0, kWaitLimit)) *gave_up = 1;
+    tc::fence_after();
+    if (split == 1) {
+      for (int j = 0; j < kTok; j += 16) {
+        int v[16];
+        tmem_ld16i(lanes + j, v);
+        if (tok0 + j < p.M) store16_any(p, c, tok0 + j, v);
+      }
+    }
+  }
+  if constexpr (Cfg::kRed > 0) {
+    if (split > 1) {
+      // column j goes to CTA j / per, which keeps [part][column][channel]
+      const int per = (kTok + split - 1) / split;
+      const int ch = (warp & 3) * 32 + lane;
+      if (warp < 4) {
+        for (int j = 0; j < kTok; j += 16) {
+          if (tok0 + j >= p.M) break;
+          int v[16];
+          tmem_ld16i(lanes + j, v);
+          int owner = j / per, at = j % per;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t dst = mapa(
+                tc::smem_u32(red + ((int)rank * per + at) * kRows + ch), (uint32_t)owner);
+            asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(dst), "r"(v[i]) : "memory");
+            if (++at == per) at = 0, ++owner;
+          }
+        }
+      }
+      cluster_sync();
+      if (warp < 4) {
+        for (int j = 0; j < per; ++j) {
+          const int64_t t = tok0 + (int64_t)rank * per + j;
+          if ((int)rank * per + j >= kTok || t >= p.M) break;
+          int acc = 0;
+          for (int r = 0; r < split; ++r) acc += red[(r * per + j) * kRows + ch];
+          if (p.dtype == SSMQ_F16)
+            store_one<__half>(p, c, t, acc);
+          else if (p.dtype == SSMQ_BF16)
+            store_one<__nv_bfloat16>(p, c, t, acc);
+          else
+            store_one<float>(p, c, t, acc);
+        }
+      }
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 5) tc::tmem_dealloc(tmem, Cfg::kCols);
+  if (threadIdx.x == 0 && *gave_up) flag_status(p.status, SSMQ_DEV_TIMEOUT);
+}
+
+// ---- many tokens: 256 channels x 256 tokens per CTA pair, persistent -----------
+// Bound: the tensor cores.  The two SMs of a pair share one 256 x 256 tile:
+// each brings 128 channels and 128 tokens per K block (half the operand
+// traffic per MMA of two separate 128 x 256 tiles), the leader issues the
+// MMAs of both.  Accumulators are double-buffered in TMEM (2 x 256 columns),
+// so four warps per CTA write tile i while the MMAs of tile i + 1 run.
+constexpr int kPairThreads = 256;  // warp 0 TMA, 1 MMA, 2 TMEM, 4-7 epilogue
+constexpr int kPairStages = 6;
+constexpr int kPairStage = 2 * kOperand;
+constexpr int kPairTok = 256, kPairCh = 256;
+constexpr int kPairSmem = 1024 + kPairStages * kPairStage + 256;
+
+// Tile i -> (channel tile, token tile): channels fastest inside a group of
+// p.group channel tiles, so that the tiles in flight share tokens and the
+// group's weights stay in L2.
+__device__ __forceinline__ void tile_at(const LinParams& p, int64_t i, int64_t& ch, int64_t& tok) {
+  const int64_t per = p.group * p.tok_tiles;
+  const int64_t g = i / per, r = i % per;
+  const int64_t left = p.ch_tiles - g * p.group;
+  const int64_t w = left < p.group ? left : p.group;
+  ch = g * p.group + r % w;
+  tok = r / w;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
+    int8_linear_pair_kernel(const __grid_constant__ CUtensorMap wmap,
+                            const __grid_constant__ CUtensorMap xmap, const LinParams p) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~1023ull);
+  uint64_t* full = reinterpret_cast<uint64_t*>(base + kPairStages * kPairStage);
+  uint64_t* empty = full + kPairStages;
+  uint64_t* acc_full = empty + kPairStages;  // [2]
+  uint64_t* acc_empty = acc_full + 2;        // [2], the leader's collect both CTAs
+  uint32_t* slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  volatile uint32_t* gave_up = slot + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cta_rank();
+  const int64_t tiles = p.tok_tiles * p.ch_tiles;
+  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPairStages; ++i) {
+      tc::mbar_init(full + i, 1);
+      tc::mbar_init(empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(acc_full + i, 1);
+      tc::mbar_init(acc_empty + i, 2 * 4);  // the epilogue warps of both CTAs
+    }
+    *gave_up = 0;
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     tc::smem_u32(slot)),
+                 "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  tc::fence_before();
+  cluster_sync();  // barriers of both CTAs exist
+  tc::fence_after();
+  const uint32_t tmem = *slot;
+
+  if (warp == 0 && lane == 0) {
+    prefetch_map(&wmap);
+    prefetch_map(&xmap);
+    int64_t i = 0;  // stage uses
+    bool ok = true;
+    for (int64_t t = pair; t < tiles && ok; t += pairs) {
+      int64_t ch, tok;
+      tile_at(p, t, ch, tok);
+      const int wrow = (int)(ch * kPairCh + rank * kRows);
+      const int xrow = (int)(tok * kPairTok + rank * kRows);
+      for (int kb = 0; kb < p.kblocks; ++kb, ++i) {
+        const int s = (int)(i % kPairStages);
+        if (i >= kPairStages &&
+            !tc::mbar_wait(empty + s, (uint32_t)(i / kPairStages - 1) & 1u, kWaitLimit)) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = mapa(tc::smem_u32(full + s), 0);
+        const uint32_t dst = tc::smem_u32(base + s * kPairStage);
+        if (rank == 0) stream::expect_tx(full + s, 2 * kPairStage);
+        tma_load_pair(dst, &wmap, kb * kBlockK, wrow, bar);
+        tma_load_pair(dst + kOperand, &xmap, kb * kBlockK, xrow, bar);
+      }
+    }
+    if (!ok) {
+      *gave_up = 1;
+      if (rank == 0)  // copies in flight land before the CTAs leave
+        for (int64_t j = i > kPairStages ? i - kPairStages : 0; j < i; ++j)
+          tc::mbar_wait(full + j % kPairStages, (uint32_t)(j / kPairStages) & 1u, kWaitLimit);
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    constexpr uint32_t idesc = idesc_i8(kPairCh, kPairTok);
+    int64_t i = 0;
+    int64_t n = 0;  // tiles of this pair
+    bool ok = true;
+    for (int64_t t = pair; t < tiles && ok; t += pairs, ++n) {
+      const int b = (int)(n & 1);
+      if (n >= 2 && !tc::mbar_wait(acc_empty + b, (uint32_t)(n / 2 - 1) & 1u, kWaitLimit)) {
+        ok = false;
+        break;
+      }
+      tc::fence_after();
+      const uint32_t d = tmem + (uint32_t)b * kPairTok;
+      for (int kb = 0; kb < p.kblocks; ++kb, ++i) {
+        const int s = (int)(i % kPairStages);
+        if (!tc::mbar_wait(full + s, (uint32_t)(i / kPairStages) & 1u, kWaitLimit)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after();
+        const uint32_t a = tc::smem_u32(base + s * kPairStage);
+        const uint64_t ad = sw128_desc(a), bd = sw128_desc(a + kOperand);
+#pragma unroll
+        for (int q = 0; q < kBlockK / 32; ++q)
+          mma_i8<2>(d, ad + 2 * q, bd + 2 * q, idesc, kb > 0 || q > 0);
+        commit_pair(empty + s);
+      }
+      commit_pair(acc_full + b);
+    }
+    if (!ok) *gave_up = 1;
+  } else if (warp >= 4) {
+    const int quarter = warp & 3;
+    int64_t n = 0;
+    for (int64_t t = pair; t < tiles; t += pairs, ++n) {
+      const int b = (int)(n & 1);
+      int64_t ch, tok;
+      tile_at(p, t, ch, tok);
+      const Channel c = channel_of(p, ch * kPairCh + rank * kRows + quarter * 32 + lane);
+      if (!tc::mbar_wait(acc_full + b, (uint32_t)(n / 2) & 1u, kWaitLimit)) {
+        *gave_up = 1;
+        break;
+      }
+      tc::fence_after();
+      const uint32_t src = tmem + (uint32_t)b * kPairTok + ((uint32_t)(quarter * 32) << 16);
+      for (int j = 0; j < kPairTok; j += 16) {
+        int v[16];
+        tmem_ld16i(src + j, v);
+        if (tok * kPairTok + j < p.M) store16_any(p, c, tok * kPairTok + j, v);
+      }
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_remote(mapa(tc::smem_u32(acc_empty + b), 0));
+    }
+  }
+  __syncwarp();
+  tc::fence_before();
+  cluster_sync();  // the pair's MMAs, copies and remote arrivals are done
+  if (warp == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  if (threadIdx.x == 0 && *gave_up) flag_status(p.status, SSMQ_DEV_TIMEOUT);
+}
+
+// ---- rows onto 16-byte boundaries -----------------------------------------------
+// Operands whose base or stride TMA cannot take are copied once to rows of a
+// multiple of 16 bytes (zero-padded): one aligned 16-byte store per thread,
+// its bytes gathered from aligned 32-bit words.
+__global__ void __launch_bounds__(256) align_rows_kernel(const int8_t* src, int64_t stride,
+                                                         int64_t rows, int64_t len, int8_t* dst,
+                                                         int64_t pitch) {
+  const int64_t per = pitch / 16;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= rows * per) return;
+  const int64_t r = i / per, c = (i % per) * 16;
+  const int8_t* s = src + r * stride + c;
+  uint32_t w[4] = {0, 0, 0, 0};
+  if (c + 16 <= len) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(s);
+    const int sh = (int)(a & 3) * 8;
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(a & ~(uintptr_t)3);
+    if (sh == 0) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = q[k];
+    } else {
+      // (the fifth word holds bytes of this row: the piece is not aligned)
+      uint32_t v = q[0];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t u = q[k + 1];
+        w[k] = __funnelshift_r(v, u, sh);
+        v = u;
+      }
+    }
+  } else {
+    for (int k = 0; k < 16; ++k)
+      if (c + k < len) w[k >> 2] |= (uint32_t)(uint8_t)s[k] << (8 * (k & 3));
+  }
+  *reinterpret_cast<uint4*>(dst + r * pitch + c) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__global__ void __launch_bounds__(256) bias_rows_kernel(const LinParams p) {
+  const int64_t n = p.M * p.N;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t t = i / p.N, c = i % p.N;
+    const float v = p.bias ? p.bias[c] : 0.0f;
+    if (p.dtype == SSMQ_F16)
+      static_cast<__half*>(p.y)[t * p.ldy + c] = __float2half_rn(v);
+    else if (p.dtype == SSMQ_BF16)
+      static_cast<__nv_bfloat16*>(p.y)[t * p.ldy + c] = __float2bfloat16_rn(v);
+    else
+      static_cast<float*>(p.y)[t * p.ldy + c] = v;
+  }
+}
+
+// ---- host ----------------------------------------------------------------------
+int64_t pitch_of(int64_t k) { return (k + 15) / 16 * 16; }
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+bool tma_rows(const void* p, int64_t rows, int64_t stride) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (rows <= 1 || stride % 16 == 0);
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                             const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                             const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// cuTensorMapEncodeTiled, looked up once per process (a driver entry point: the
+// library does not link libcuda)
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+
+cudaError_t encode(CUtensorMap* map, const void* p, int64_t rows, int64_t k, int64_t stride,
+                   int box_rows) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows};
+  // (one row: its stride is never used, but has to be a multiple of 16)
+  const cuuint64_t strides[1] = {(cuuint64_t)(rows <= 1 ? pitch_of(k) : stride)};
+  const cuuint32_t box[2] = {(cuuint32_t)kBlockK, (cuuint32_t)box_rows};
+  const cuuint32_t one[2] = {1, 1};
+  const CUresult r =
+      fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, box, one,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int kTok>
+cudaError_t launch_split(const CUtensorMap& wmap, const CUtensorMap& xmap, LinParams p,
+                         cudaStream_t st) {
+  using Cfg = SplitCfg<kTok>;
+  p.ch_tiles = (p.N + kRows - 1) / kRows;
+  p.tok_tiles = (p.M + kTok - 1) / kTok;
+  const int64_t tiles = p.ch_tiles * p.tok_tiles;
+  int split = 1;
+  // parts of K while the CTAs fit the SMs once and a part keeps four K blocks
+  if (Cfg::kRed > 0)
+    while (split < kMaxSplit && tiles * split * 2 <= sm_count() && p.kblocks >= 8 * split)
+      split *= 2;
+  static_assert(Cfg::kSmem <= 227 * 1024, "shared memory");
+  const cudaError_t e =
+      cudaFuncSetAttribute(int8_linear_split_kernel<kTok>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * split));
+  cfg.blockDim = dim3(kSplitThreads);
+  cfg.dynamicSmemBytes = Cfg::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)split;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = split > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, int8_linear_split_kernel<kTok>, wmap, xmap, p, split);
+}
+
+}  // namespace
+
+size_t int8_linear_workspace_bytes(const ssmq_linear_args& a) {
+  size_t n = 0;
+  if (a.tokens <= 0 || a.out_features <= 0 || a.in_features <= 0) return 0;
+  if (!tma_rows(a.x, a.tokens, a.x_stride))
+    n += up256((size_t)a.tokens * pitch_of(a.in_features));
+  if (!tma_rows(a.w, a.out_features, a.w_stride))
+    n += up256((size_t)a.out_features * pitch_of(a.in_features));
+  return n;
+}
+
+cudaError_t launch_int8_linear(const ssmq_linear_args& a, void* ws, cudaStream_t st) {
+  LinParams p = {};
+  p.M = a.tokens;
+  p.N = a.out_features;
+  p.kblocks = (int)((a.in_features + kBlockK - 1) / kBlockK);
+  p.xs = a.x_scale;
+  p.ws = a.w_scale;
+  p.bias = a.bias;
+  p.y = a.y;
+  p.ldy = a.y_stride;
+  p.dtype = a.dtype;
+  p.status = a.status;
+  if (p.kblocks == 0) {
+    const int64_t n = (p.M * p.N + 255) / 256, most = (int64_t)sm_count() * 8;
+    bias_rows_kernel<<<(unsigned)(n < most ? n : most), 256, 0, st>>>(p);
+    return cudaGetLastError();
+  }
+  const int8_t* x = a.x;
+  const int8_t* w = a.w;
+  int64_t xst = a.x_stride, wst = a.w_stride;
+  const int64_t pitch = pitch_of(a.in_features);
+  uint8_t* room = static_cast<uint8_t*>(ws);
+  auto align_rows = [&](const int8_t*& t, int64_t& stride, int64_t rows) {
+    int8_t* dst = reinterpret_cast<int8_t*>(room);
+    const int64_t n = rows * (pitch / 16);
+    align_rows_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(t, stride, rows, a.in_features,
+                                                                   dst, pitch);
+    room += up256((size_t)rows * pitch);
+    t = dst;
+    stride = pitch;
+    return cudaGetLastError();
+  };
+  cudaError_t e;
+  if (!tma_rows(x, p.M, xst) && (e = align_rows(x, xst, p.M)) != cudaSuccess) return e;
+  if (!tma_rows(w, p.N, wst) && (e = align_rows(w, wst, p.N)) != cudaSuccess) return e;
+
+  // Enough 256 x 256 tiles for every CTA pair: the pair kernel.  Fewer: smaller
+  // tiles, so that more SMs take part.
+  const int sms = sm_count();
+  const int64_t pair_tiles = ((p.M + kPairTok - 1) / kPairTok) * ((p.N + kPairCh - 1) / kPairCh);
+  const bool pair = p.M > 128 && pair_tiles >= sms / 2;
+  int tok = pair ? kRows : 128;
+  if (!pair && p.M <= 64) tok = p.M <= 16 ? 16 : (p.M <= 32 ? 32 : 64);
+  CUtensorMap wmap, xmap;
+  if ((e = encode(&wmap, w, p.N, a.in_features, wst, kRows)) != cudaSuccess) return e;
+  if ((e = encode(&xmap, x, p.M, a.in_features, xst, tok)) != cudaSuccess) return e;
+  if (!pair) {
+    switch (tok) {
+      case 16: return launch_split<16>(wmap, xmap, p, st);
+      case 32: return launch_split<32>(wmap, xmap, p, st);
+      case 64: return launch_split<64>(wmap, xmap, p, st);
+      default: return launch_split<128>(wmap, xmap, p, st);
+    }
+  }
+  p.tok_tiles = (p.M + kPairTok - 1) / kPairTok;
+  p.ch_tiles = (p.N + kPairCh - 1) / kPairCh;
+  p.group = 16;
+  e = cudaFuncSetAttribute(int8_linear_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kPairSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t pairs = pair_tiles < sms / 2 ? pair_tiles : sms / 2;
+  int8_linear_pair_kernel<<<(unsigned)(2 * pairs), kPairThreads, kPairSmem, st>>>(wmap, xmap, p);
+  return cudaGetLastError();
+}
+
+}  // namespace ssmq

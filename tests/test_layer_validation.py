@@ -28,7 +28,8 @@ def _c_name(field):
 
 
 def test_struct_layout_matches_header(tmp_path):
-    structs = ((N.NormArgs, "ssmq_norm_args"), (N.GatedArgs, "ssmq_gated_args"),
+    structs = ((N.NormArgs, "ssmq_norm_args"), (N.LinearArgs, "ssmq_linear_args"),
+               (N.GatedArgs, "ssmq_gated_args"),
                (N.GatedGradArgs, "ssmq_gated_grad_args"))
     prog = ["#include <stdio.h>", "#include <stddef.h>", '#include "ssmq.h"', "int main(void){"]
     for cls, cname in structs:
@@ -75,6 +76,42 @@ def test_norm(L):
     assert S(residual_out=A + STEP, **r) == N.ERR_INVALID_ARG         # the codes
     assert S(y=A, y_stride=64) == N.ERR_INVALID_ARG
     assert S(tokens=0, x=None) == N.OK
+
+
+def test_linear(L, monkeypatch):
+    base = dict(tokens=8, out_features=24, in_features=64, dtype=N.F16, x=A, x_stride=64,
+                x_scale=A + STEP, w=A + 2 * STEP, w_stride=64, w_scale=A + 3 * STEP,
+                y=A + 4 * STEP, y_stride=24)
+    args = lambda **kw: C.byref(N.LinearArgs(**{**base, **kw}))
+    S = lambda ws=None, nb=0, **kw: L.ssmq_int8_linear(args(**kw), ws, nb, None)
+    W = lambda **kw: L.ssmq_int8_linear_workspace_size(args(**kw))
+    assert L.ssmq_int8_linear(None, None, 0, None) == N.ERR_INVALID_ARG
+    assert S(dtype=9) == N.ERR_INVALID_ARG
+    assert S(tokens=-1) == N.ERR_INVALID_ARG
+    assert S(in_features=131072, x_stride=1 << 18, w_stride=1 << 18) == N.ERR_UNSUPPORTED
+    assert S(tokens=1 << 31) == N.ERR_UNSUPPORTED
+    assert S(x=None) == N.ERR_INVALID_ARG
+    assert S(w_scale=None) == N.ERR_INVALID_ARG
+    assert S(x_scale=A + STEP + 1) == N.ERR_ALIGNMENT
+    assert S(x_stride=63) == N.ERR_INVALID_ARG
+    assert S(y_stride=23) == N.ERR_INVALID_ARG
+    assert S(y=A + 4 * STEP + 1) == N.ERR_ALIGNMENT
+    assert S(y=A + 64) == N.ERR_INVALID_ARG and "y overlaps x" in N.ssmq_last_error()
+    assert S(w_stride=1 << 41) == N.ERR_UNSUPPORTED
+    assert S(tokens=0, x=None) == N.OK and S(out_features=0, w=None) == N.OK
+    # the workspace rule: only rows that are off 16-byte boundaries are copied
+    assert W() == 0 and W(x=A + 16) == 0 and W(tokens=1, x_stride=3) == 0
+    assert W(x=A + 1) == 512 and W(w_stride=65) == 24 * 64
+    assert W(x_stride=70, w=A + 2 * STEP + 8) == 512 + 24 * 64
+    assert W(in_features=50) == 0 and W(in_features=50, x_stride=50) == 512
+    assert L.ssmq_int8_linear_workspace_size(None) == 0
+    assert S(x=A + 1) == N.ERR_INVALID_ARG and "workspace" in N.ssmq_last_error()
+    assert S(x=A + 1, ws=A + 8 * STEP, nb=511) == N.ERR_INVALID_ARG
+    assert S(x=A + 1, ws=A + 8 * STEP + 16, nb=512) == N.ERR_ALIGNMENT
+    assert S(x=A + 1, ws=A + 2 * STEP, nb=512) == N.ERR_INVALID_ARG   # on w
+    monkeypatch.setenv("SSMQ_FAULT_INJECT", "ssmq_int8_linear")
+    assert S() == N.ERR_CUDA
+    assert S(x=A + 1, ws=A + 8 * STEP, nb=512) == N.ERR_CUDA
 
 
 def _gated(**kw):
@@ -165,6 +202,11 @@ def test_python_front_end_refusals():
         api.rms_norm_quantize(x)  # not on a GPU
     with pytest.raises(ValueError):
         api.rms_norm_quantize(x.double())
+    q = torch.zeros(4, 16, dtype=torch.int8)
+    with pytest.raises(ValueError):
+        api.int8_linear(q, torch.ones(4), q, torch.ones(4))
+    with pytest.raises(ValueError):
+        api.int8_linear(q, torch.ones(4), q, torch.ones(4), dtype=torch.int32)
     with pytest.raises(ValueError):
         api.gated_scan(x, x)
     with pytest.raises(ValueError):
