@@ -8,6 +8,7 @@ the import fails.
 """
 import ctypes as C
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libssmq.so")
@@ -149,13 +150,13 @@ SIGNATURES = {
                                            _vp]),
     "ssmq_softedge_calibrate_noalloc": (_i32, [_vp, _i32, _i64, C.c_double, C.c_double, _f32,
                                                _vp, _vp]),
-    "ssmq_rms_norm_quantize": (_i32, [C.POINTER(NormArgs), _vp]),
-    "ssmq_int8_linear_workspace_size": (C.c_size_t, [C.POINTER(LinearArgs)]),
-    "ssmq_int8_linear": (_i32, [C.POINTER(LinearArgs), _vp, C.c_size_t, _vp]),
+    "ssmq_rms_norm_quantize": (_i32, [_vp, _vp]),
+    "ssmq_int8_linear_workspace_size": (C.c_size_t, [_vp]),
+    "ssmq_int8_linear": (_i32, [_vp, _vp, C.c_size_t, _vp]),
     "ssmq_gated_scan_state_steps": (_i32, []),
-    "ssmq_gated_scan": (_i32, [C.POINTER(GatedArgs), _vp]),
-    "ssmq_gated_scan_backward": (_i32, [C.POINTER(GatedGradArgs), _vp]),
-    "ssmq_gated_update": (_i32, [C.POINTER(GatedArgs), _vp]),
+    "ssmq_gated_scan": (_i32, [_vp, _vp]),
+    "ssmq_gated_scan_backward": (_i32, [_vp, _vp]),
+    "ssmq_gated_update": (_i32, [_vp, _vp]),
     "ssmq_probe_ex2": (_i32, [_i32, _vp, C.POINTER(C.c_int64), _vp]),
     "ssmq_last_error": (C.c_char_p, []),
     "ssmq_version": (_i32, []),
@@ -320,52 +321,51 @@ def ssmq_state_chain(h_end, dec, n_parts, units, elems, h_out, stream=None):
                                   _stream(stream)))
 
 
-def _struct(cls, fields):
-    """An argument struct from keywords; unlike _fill, tensors become addresses
-    in one pass and the struct's own constructor checks the names."""
-    for k, v in fields.items():
-        if hasattr(v, "data_ptr"):
-            fields[k] = v.data_ptr()
-    return cls(**fields)
+# The calls below serve single tokens, where the host's time per call counts:
+# they take every field of the argument struct in its order (tensors as
+# addresses, 0 for NULL) and pack the struct in one step.
+_NORM = struct.Struct("=qqifQqQqQQqQqQqQQ").pack
+_LINEAR = struct.Struct("=qqqi4xQqQQqQQQqQ").pack
+_GATED = struct.Struct("=qqqi4x" + 4 * "Qqq" + "QQQQ").pack
+_GATED_GRAD = struct.Struct("=qqqi4x" + 7 * "Qqq" + "QQQQ").pack
 
 
-def ssmq_rms_norm_quantize(stream=None, **fields):
-    """Fields of ssmq_norm_args as keywords (tensors for pointer fields)."""
-    a = _struct(NormArgs, fields)
-    _check(lib().ssmq_rms_norm_quantize(C.byref(a), _stream(stream)))
+def ssmq_rms_norm_quantize(stream, *fields):
+    status = lib().ssmq_rms_norm_quantize(_NORM(*fields), stream)
+    if status:
+        _check(status)
 
 
-def ssmq_int8_linear_workspace_size(**fields):
-    return int(lib().ssmq_int8_linear_workspace_size(C.byref(_struct(LinearArgs, fields))))
+def ssmq_int8_linear_workspace_size(*fields):
+    return lib().ssmq_int8_linear_workspace_size(_LINEAR(*fields))
 
 
-def ssmq_int8_linear(workspace=None, ws_bytes=0, stream=None, **fields):
-    """Fields of ssmq_linear_args as keywords (tensors for pointer fields)."""
-    a = _struct(LinearArgs, fields)
-    _check(lib().ssmq_int8_linear(C.byref(a), ptr(workspace), ws_bytes, _stream(stream)))
+def ssmq_int8_linear(stream, workspace, ws_bytes, *fields):
+    status = lib().ssmq_int8_linear(_LINEAR(*fields), workspace, ws_bytes, stream)
+    if status:
+        _check(status)
 
 
 def ssmq_gated_scan_state_steps():
-    return int(lib().ssmq_gated_scan_state_steps())
+    return lib().ssmq_gated_scan_state_steps()
 
 
-def ssmq_gated_scan(stream=None, **fields):
-    """Fields of ssmq_gated_args as keywords; the strides of tensor x are
-    x_batch_stride and x_row_stride."""
-    a = _struct(GatedArgs, fields)
-    _check(lib().ssmq_gated_scan(C.byref(a), _stream(stream)))
+def ssmq_gated_scan(stream, *fields):
+    status = lib().ssmq_gated_scan(_GATED(*fields), stream)
+    if status:
+        _check(status)
 
 
-def ssmq_gated_scan_backward(stream=None, **fields):
-    """Fields of ssmq_gated_grad_args as keywords (strides as ssmq_gated_scan)."""
-    a = _struct(GatedGradArgs, fields)
-    _check(lib().ssmq_gated_scan_backward(C.byref(a), _stream(stream)))
+def ssmq_gated_scan_backward(stream, *fields):
+    status = lib().ssmq_gated_scan_backward(_GATED_GRAD(*fields), stream)
+    if status:
+        _check(status)
 
 
-def ssmq_gated_update(stream=None, **fields):
-    """Fields of ssmq_gated_args as keywords; h_final is the state."""
-    a = _struct(GatedArgs, fields)
-    _check(lib().ssmq_gated_update(C.byref(a), _stream(stream)))
+def ssmq_gated_update(stream, *fields):
+    status = lib().ssmq_gated_update(_GATED(*fields), stream)
+    if status:
+        _check(status)
 
 
 def ssmq_state_update_w8(stream=None, **fields):

@@ -6,6 +6,7 @@ of the computation runs in the CUDA library.  Layouts and semantics are those
 of include/ssmq.h.
 """
 import contextlib
+import math
 
 import torch
 
@@ -50,7 +51,7 @@ def _in(t, name, dtypes, numel, device):
 def _on(device):
     """Launches go to the device that holds the tensors (and its current
     stream), whatever device is current in the caller."""
-    if device.type == "cuda" and device.index != torch.cuda.current_device():
+    if device.type == "cuda":
         return torch.cuda.device(device)
     return contextlib.nullcontext()
 
@@ -625,15 +626,50 @@ def softedge_calibrate_noalloc(src, thresholds, *, q_lo=5.0, q_hi=99.9, alpha=1.
 _DTYPE_IDS = {torch.float32: N.F32, torch.float16: N.F16, torch.bfloat16: N.BF16}
 
 
+def _call(device, entry, *fields):
+    """entry(stream, *fields) on ``device`` and its current stream."""
+    i = device.index
+    if i == torch.cuda.current_device():
+        entry(torch._C._cuda_getCurrentRawStream(i), *fields)
+    else:
+        with torch.cuda.device(device):
+            entry(torch._C._cuda_getCurrentRawStream(i), *fields)
+
+
+def _cuda(t, name, dim=None):
+    """The device and type id of a call's leading tensor."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype not in _DTYPE_IDS or (dim is not None and t.dim() != dim):
+        raise ValueError("%s must be a %sfloat16, bfloat16 or float32 tensor (got %s of %s)"
+                         % (name, "" if dim is None else "%d-dimensional " % dim, t.dtype,
+                            tuple(t.shape)))
+    return t.device, _DTYPE_IDS[t.dtype]
+
+
+def _dense(t, name, dtype, numel, device):
+    """Address of a dense tensor of ``numel`` elements, 0 for None."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or t.numel() != numel or t.device != device or not t.is_contiguous():
+        _in(t, name, dtype, numel, device)
+    return t.data_ptr()
+
+
+def _status_ptr(t, device):
+    _status(t, device)
+    return 0 if t is None else t.data_ptr()
+
+
 def _row_tensor(t, name, shape, dtype, device):
     """A tensor of contiguous rows (..., d) for the strided-row operators: of
     this shape, dtype and device, its last dimension contiguous."""
-    if t.device != device or device.type != "cuda":
-        raise ValueError("%s must be a CUDA tensor on %s" % (name, device))
+    if t.device != device:
+        raise ValueError("%s must be on %s" % (name, device))
     if t.dtype != dtype or t.shape != shape:
         raise ValueError("%s must be %s of shape %s (got %s of %s)"
                          % (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    if t.stride(-1) != 1 and shape[-1] > 1:
         raise ValueError("%s: the last dimension must be contiguous" % name)
 
 
@@ -668,45 +704,43 @@ def rms_norm_quantize(x, weight=None, *, residual=None, eps=1e-5, residual_out=N
     float32 feed int8_linear.  residual_out may be x or residual itself (in
     place).  want_codes=False leaves the codes out (codes and scales are then
     None).  Codes that the call allocates lie on 16-byte rows."""
-    d = x.shape[-1]
-    dv, dt = x.device, x.dtype
-    if dt not in _DTYPE_IDS:
-        raise ValueError("x must be float16, bfloat16 or float32 (got %s)" % dt)
-    shape, lead = x.shape, x.shape[:-1]
+    dv, kind = _cuda(x, "x")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must have at least one channel")
+    shape, dt = x.shape, x.dtype
+    d = shape[-1]
+    tokens = x.numel() // d
     xp, xs = _flat_rows(x, "x", shape, dt, dv)
-    tokens = 1
-    for v in lead:
-        tokens *= v
-    _in(weight, "weight", torch.float32, d, dv)
-    _status(status, dv)
-    with _on(dv):
-        f = dict(tokens=tokens, dim=d, dtype=_DTYPE_IDS[dt], eps=eps, x=xp, x_stride=xs,
-                 weight=weight, status=status)
-        out = ()
-        if residual is not None:
-            f["residual"], f["residual_stride"] = _flat_rows(residual, "residual", shape, dt, dv)
-            if residual_out is None:
-                residual_out = torch.empty(shape, dtype=dt, device=dv)
-            out = (residual_out,)
-        if residual_out is not None:
-            f["residual_out"], f["residual_out_stride"] = _flat_rows(residual_out, "residual_out",
-                                                                     shape, dt, dv)
-        if want_y or y is not None:
-            if y is None:
-                y = torch.empty(shape, dtype=dt, device=dv)
-            f["y"], f["y_stride"] = _flat_rows(y, "y", shape, dt, dv)
-            out += (y,)
-        if want_codes or codes is not None or scales is not None:
-            if codes is None:
-                codes = torch.empty((*lead, (d + 15) // 16 * 16), dtype=torch.int8, device=dv)
-                if d % 16:
-                    codes = codes[..., :d]
-            if scales is None:
-                scales = torch.empty(lead, dtype=torch.float32, device=dv)
-            _out(scales, "scales", torch.float32, tokens, dv)
-            f["codes"], f["codes_stride"] = _flat_rows(codes, "codes", shape, torch.int8, dv)
-            f["scales"] = scales
-        N.ssmq_rms_norm_quantize(torch.cuda.current_stream().cuda_stream, **f)
+    wp = _dense(weight, "weight", torch.float32, d, dv)
+    rp = rs = op = os = yp = ys = qp = qs = sp = 0
+    out = ()
+    if residual is not None:
+        rp, rs = _flat_rows(residual, "residual", shape, dt, dv)
+        if residual_out is None:
+            residual_out = torch.empty(shape, dtype=dt, device=dv)
+        out = (residual_out,)
+    if residual_out is not None:
+        op, os = _flat_rows(residual_out, "residual_out", shape, dt, dv)
+    if want_y or y is not None:
+        if y is None:
+            y = torch.empty(shape, dtype=dt, device=dv)
+        yp, ys = _flat_rows(y, "y", shape, dt, dv)
+        out += (y,)
+    if want_codes or codes is not None or scales is not None:
+        lead = shape[:-1]
+        if codes is None:
+            if d % 16:
+                codes = torch.empty((*lead, (d + 15) // 16 * 16), dtype=torch.int8,
+                                    device=dv)[..., :d]
+            else:
+                codes = torch.empty(shape, dtype=torch.int8, device=dv)
+        if scales is None:
+            scales = torch.empty(lead, dtype=torch.float32, device=dv)
+        qp, qs = _flat_rows(codes, "codes", shape, torch.int8, dv)
+        _out(scales, "scales", torch.float32, tokens, dv)
+        sp = scales.data_ptr()
+    _call(dv, N.ssmq_rms_norm_quantize, tokens, d, kind, eps, xp, xs, rp, rs, wp, op, os, yp, ys,
+          qp, qs, sp, _status_ptr(status, dv))
     return (codes, scales) + out
 
 
@@ -719,7 +753,6 @@ def int8_linear(x, x_scale, w, w_scale, *, bias=None, out=None, dtype=None, work
     16-byte boundaries (such as the codes of rms_norm_quantize) are read in
     place; others are first copied into ``workspace`` (uint8 bytes on the
     device, allocated when not given)."""
-    dv, K = x.device, x.shape[-1]
     if out is not None:
         if dtype is not None and dtype != out.dtype:
             raise ValueError("dtype %s differs from out's %s" % (dtype, out.dtype))
@@ -728,75 +761,72 @@ def int8_linear(x, x_scale, w, w_scale, *, bias=None, out=None, dtype=None, work
         dtype = torch.float16
     if dtype not in _DTYPE_IDS:
         raise ValueError("the output must be float16, bfloat16 or float32 (got %s)" % dtype)
-    xp, xst = _flat_rows(x, "x", x.shape, torch.int8, dv)
-    if w.dim() != 2:
-        raise ValueError("w must be (out_features, in_features)")
-    n = w.shape[0]
+    if not x.is_cuda or x.dim() < 1 or w.dim() != 2:
+        raise ValueError("x (..., in_features) and w (out_features, in_features) must be CUDA "
+                         "tensors")
+    dv, shape = x.device, x.shape
+    K, n = shape[-1], w.shape[0]
+    xp, xst = _flat_rows(x, "x", shape, torch.int8, dv)
     wp, wst = _flat_rows(w, "w", (n, K), torch.int8, dv)
-    lead = x.shape[:-1]
-    tokens = 1
-    for v in lead:
-        tokens *= v
-    _in(x_scale, "x_scale", torch.float32, tokens, dv)
-    _in(w_scale, "w_scale", torch.float32, n, dv)
-    _in(bias, "bias", torch.float32, n, dv)
-    _status(status, dv)
-    with _on(dv):
-        if out is None:
-            out = torch.empty((*lead, n), dtype=dtype, device=dv)
-        yp, yst = _flat_rows(out, "out", (*lead, n), dtype, dv)
-        f = dict(tokens=tokens, out_features=n, in_features=K, dtype=_DTYPE_IDS[dtype], x=xp,
-                 x_stride=xst, x_scale=x_scale, w=wp, w_stride=wst, w_scale=w_scale, bias=bias,
-                 y=yp, y_stride=yst, status=status)
-        ws, wptr = 0, None
-        if (xp | wp | xst | wst) % 16:
-            ws = N.ssmq_int8_linear_workspace_size(**f)
-            _workspace(workspace, ws, dv)
-            if ws and workspace is None:
+    tokens = x_scale.numel()
+    oshape = (*shape[:-1], n)
+    xsp = _dense(x_scale, "x_scale", torch.float32, math.prod(shape[:-1]), dv)
+    wsp = _dense(w_scale, "w_scale", torch.float32, n, dv)
+    bp = _dense(bias, "bias", torch.float32, n, dv)
+    if out is None:
+        out = torch.empty(oshape, dtype=dtype, device=dv)
+    yp, yst = _flat_rows(out, "out", oshape, dtype, dv)
+    f = (tokens, n, K, _DTYPE_IDS[dtype], xp, xst, xsp, wp, wst, wsp, bp, yp, yst,
+         _status_ptr(status, dv))
+    ws = wptr = 0
+    if (xp | wp | xst | wst) % 16:
+        ws = N.ssmq_int8_linear_workspace_size(*f)
+        _workspace(workspace, ws, dv)
+        if ws:
+            if workspace is None:
                 workspace = torch.empty(ws + 256, dtype=torch.uint8, device=dv)
-            wptr = (workspace.data_ptr() + 255) // 256 * 256 if ws else None
-        N.ssmq_int8_linear(wptr, ws, torch.cuda.current_stream().cuda_stream, **f)
+            wptr = (workspace.data_ptr() + 255) // 256 * 256
+    _call(dv, N.ssmq_int8_linear, wptr, ws, *f)
     return out
 
 
 # ---- gated linear recurrence ----------------------------------------------------
 
-def _gated_rows(f, t, name, shape, dtype, device):
-    """Address and strides of a (b, L, d) tensor into the call's fields."""
+def _gated_rows(t, name, shape, dtype, device):
+    """(address, batch stride, row stride) of a (b, L, d) tensor."""
     _row_tensor(t, name, shape, dtype, device)
     st = t.stride()
-    f[name] = t.data_ptr()
-    f[name + "_batch_stride"] = st[0]
-    f[name + "_row_stride"] = st[1]
+    return t.data_ptr(), st[0], st[1]
+
+
+_NONE = (0, 0, 0)
+
+
+def _saved_states(L):
+    k = N.ssmq_gated_scan_state_steps()
+    return (L + k - 1) // k
 
 
 def _gated_scan(v, g, z, h0, lengths, y, h_final, states, return_state, save_states):
-    if v.dim() != 3 or v.dtype not in _DTYPE_IDS:
-        raise ValueError("v must be a (b, L, d) float16, bfloat16 or float32 tensor")
-    shape, dv, dt = v.shape, v.device, v.dtype
+    dv, kind = _cuda(v, "v", 3)
+    shape, dt = v.shape, v.dtype
     b, L, d = shape
-    _in(h0, "h0", torch.float32, b * d, dv)
-    _in(lengths, "lengths", torch.int32, b, dv)
-    f = dict(batch=b, seqlen=L, dim=d, dtype=_DTYPE_IDS[dt], h0=h0, lengths=lengths)
-    _gated_rows(f, v, "v", shape, dt, dv)
-    _gated_rows(f, g, "g", shape, dt, dv)
-    if z is not None:
-        _gated_rows(f, z, "z", shape, dt, dv)
-    with _on(dv):
-        if y is None:
-            y = torch.empty(shape, dtype=dt, device=dv)
-        _gated_rows(f, y, "y", shape, dt, dv)
-        if h_final is None and return_state:
-            h_final = torch.empty((b, d), dtype=torch.float32, device=dv)
-        _out(h_final, "h_final", torch.float32, b * d, dv)
-        if save_states or states is not None:
-            k = N.ssmq_gated_scan_state_steps()
-            n = (L + k - 1) // k
-            if states is None:
-                states = torch.empty((b, n, d), dtype=torch.float32, device=dv)
-            _out(states, "states", torch.float32, b * n * d, dv)
-        f["h_final"], f["states"] = h_final, states
-        N.ssmq_gated_scan(torch.cuda.current_stream().cuda_stream, **f)
+    if y is None:
+        y = torch.empty(shape, dtype=dt, device=dv)
+    if h_final is None and return_state:
+        h_final = torch.empty((b, d), dtype=torch.float32, device=dv)
+    stp = 0
+    if save_states or states is not None:
+        n = _saved_states(L)
+        if states is None:
+            states = torch.empty((b, n, d), dtype=torch.float32, device=dv)
+        stp = _dense(states, "states", torch.float32, b * n * d, dv)
+    _call(dv, N.ssmq_gated_scan, b, L, d, kind, *_gated_rows(v, "v", shape, dt, dv),
+          *_gated_rows(g, "g", shape, dt, dv),
+          *(_NONE if z is None else _gated_rows(z, "z", shape, dt, dv)),
+          *_gated_rows(y, "y", shape, dt, dv), _dense(h0, "h0", torch.float32, b * d, dv),
+          _dense(h_final, "h_final", torch.float32, b * d, dv), stp,
+          _dense(lengths, "lengths", torch.int32, b, dv))
     return y, h_final, states
 
 
@@ -815,7 +845,7 @@ class _GatedScan(torch.autograd.Function):
         v, g, z, lengths, states = ctx.saved_tensors
         if dy.stride(-1) != 1 or (v.shape[1] > 1 and dy.stride(1) < v.shape[2]):
             dy = dy.contiguous()  # (an expanded gradient, as of a sum)
-        dv, dg, dz, dh0 = gated_scan_backward(dy.to(v.dtype), v, g, states, z=z,
+        dv, dg, dz, dh0 = gated_scan_backward(dy, v, g, states, z=z,
                                               dh_final=dh_final.contiguous(), lengths=lengths)
         return dv, dg, dz, dh0 if ctx.needs_input_grad[3] else None, None
 
@@ -833,7 +863,9 @@ def gated_scan(v, g, *, z=None, h0=None, lengths=None, y=None, h_final=None, sta
     reads (or that are written into ``states`` when it is given).  When an
     input requires a gradient, the result is differentiable; the caller's
     output tensors are then not accepted."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (v, g, z, h0)):
+    if torch.is_grad_enabled() and (v.requires_grad or g.requires_grad or
+                                    (z is not None and z.requires_grad) or
+                                    (h0 is not None and h0.requires_grad)):
         if not (y is None and h_final is None and states is None and not save_states):
             raise ValueError("y, h_final, states and save_states are for inputs without "
                              "requires_grad")
@@ -850,34 +882,27 @@ def gated_scan_backward(dy, v, g, states, *, z=None, dh_final=None, lengths=None
     (b, L, d) and dh_final (b, d) float32 or None are the gradients of its
     outputs; dz is None without z.  Outputs may be given; dv, dg and dz may be
     exactly v, g, z or dy (each a different one)."""
-    if v.dim() != 3 or v.dtype not in _DTYPE_IDS:
-        raise ValueError("v must be a (b, L, d) float16, bfloat16 or float32 tensor")
-    shape, dvc, dt = v.shape, v.device, v.dtype
+    dev, kind = _cuda(v, "v", 3)
+    shape, dt = v.shape, v.dtype
     b, L, d = shape
-    k = N.ssmq_gated_scan_state_steps()
-    _in(states, "states", torch.float32, b * ((L + k - 1) // k) * d, dvc)
-    _in(dh_final, "dh_final", torch.float32, b * d, dvc)
-    _in(lengths, "lengths", torch.int32, b, dvc)
-    _out(dh0, "dh0", torch.float32, b * d, dvc)
-    f = dict(batch=b, seqlen=L, dim=d, dtype=_DTYPE_IDS[dt], states=states, dh_final=dh_final,
-             lengths=lengths)
     if z is None and dz is not None:
         raise ValueError("dz without z")
-    with _on(dvc):
-        if dv is None:
-            dv = torch.empty(shape, dtype=dt, device=dvc)
-        if dg is None:
-            dg = torch.empty(shape, dtype=dt, device=dvc)
-        if z is not None and dz is None:
-            dz = torch.empty(shape, dtype=dt, device=dvc)
-        if dh0 is None:
-            dh0 = torch.empty((b, d), dtype=torch.float32, device=dvc)
-        f["dh0"] = dh0
-        for t, name in ((v, "v"), (g, "g"), (z, "z"), (dy, "dy"), (dv, "dv"), (dg, "dg"),
-                        (dz, "dz")):
-            if t is not None:
-                _gated_rows(f, t, name, shape, dt, dvc)
-        N.ssmq_gated_scan_backward(torch.cuda.current_stream().cuda_stream, **f)
+    sp = _dense(states, "states", torch.float32, b * _saved_states(L) * d, dev)
+    if dv is None:
+        dv = torch.empty(shape, dtype=dt, device=dev)
+    if dg is None:
+        dg = torch.empty(shape, dtype=dt, device=dev)
+    if z is not None and dz is None:
+        dz = torch.empty(shape, dtype=dt, device=dev)
+    if dh0 is None:
+        dh0 = torch.empty((b, d), dtype=torch.float32, device=dev)
+    rows = []
+    for t, name in ((v, "v"), (g, "g"), (z, "z"), (dy, "dy"), (dv, "dv"), (dg, "dg"), (dz, "dz")):
+        rows += _NONE if t is None else _gated_rows(t, name, shape, dt, dev)
+    _call(dev, N.ssmq_gated_scan_backward, b, L, d, kind, *rows, sp,
+          _dense(dh_final, "dh_final", torch.float32, b * d, dev),
+          _dense(dh0, "dh0", torch.float32, b * d, dev),
+          _dense(lengths, "lengths", torch.int32, b, dev))
     return dv, dg, dz, dh0
 
 
@@ -885,19 +910,20 @@ def gated_update(state, v, g, *, z=None, y=None):
     """One step of the gated recurrence in place on ``state`` (b, d) float32;
     v, g, z (b, d) with contiguous channels.  Returns y (b, d) in v's dtype
     (y may be z itself)."""
-    if v.dim() != 2 or v.dtype not in _DTYPE_IDS:
-        raise ValueError("v must be a (b, d) float16, bfloat16 or float32 tensor")
-    shape, dv, dt = v.shape, v.device, v.dtype
+    dv, kind = _cuda(v, "v", 2)
+    shape, dt = v.shape, v.dtype
     b, d = shape
-    _out(state, "state", torch.float32, b * d, dv)
-    f = dict(batch=b, seqlen=1, dim=d, dtype=_DTYPE_IDS[dt], h_final=state)
-    with _on(dv):
-        if y is None:
-            y = torch.empty(shape, dtype=dt, device=dv)
-        for t, name in ((v, "v"), (g, "g"), (z, "z"), (y, "y")):
-            if t is not None:
-                _row_tensor(t, name, shape, dt, dv)
-                f[name] = t.data_ptr()
-                f[name + "_batch_stride"] = t.stride(0)
-        N.ssmq_gated_update(torch.cuda.current_stream().cuda_stream, **f)
+    if y is None:
+        y = torch.empty(shape, dtype=dt, device=dv)
+    if state is None:
+        raise ValueError("state is required")
+    rows = []
+    for t, name in ((v, "v"), (g, "g"), (z, "z"), (y, "y")):
+        if t is None:
+            rows += _NONE
+        else:
+            _row_tensor(t, name, shape, dt, dv)
+            rows += (t.data_ptr(), t.stride(0), d)
+    _call(dv, N.ssmq_gated_update, b, 1, d, kind, *rows, 0,
+          _dense(state, "state", torch.float32, b * d, dv), 0, 0)
     return y

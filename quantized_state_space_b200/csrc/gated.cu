@@ -4,9 +4,9 @@
 // The recurrence is the selective scan's (Quamba2 abstract) with one state per
 // channel and the decay as an input.
 //
-// Bound: HBM (v, g, z in, y out).  The inputs are read once: a tile's steps
+// Bound: HBM (v, g, z in, y out).  The inputs are read once: a tile's gates
 // stay in registers while the carried states are exchanged (gated.cuh), and
-// the next round's loads are in flight meanwhile.
+// the next round's rows are copied into shared memory meanwhile.
 #include "gated.cuh"
 
 namespace ssmq {
@@ -26,7 +26,8 @@ struct ScanParams {
 };
 
 template <typename T, bool kVec, int kLanes, bool kGate>
-__global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4)
+    gated_scan_kernel(const ScanParams p) {
   __shared__ Shared<kLanes> sh;
   using TileT = Tile<kLanes>;
   const uint32_t size = cluster_size(), rank = cluster_rank();
@@ -34,8 +35,10 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(const ScanParam
   const int64_t seq = unit / p.blocks, blk = unit % p.blocks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / kLanes, l = lane % kLanes;
-  const int64_t c0 = blk * TileT::kChannels + (kVec ? 2 * l : l);
+  int64_t c0 = blk * TileT::kChannels + (kVec ? 2 * l : l);
   const bool in0 = c0 < p.d, in1 = c0 + (kVec ? 1 : kLanes) < p.d;
+  const int next = kVec ? 1 : (in1 ? kLanes : 0);
+  if (!in0) c0 = 0;
   int64_t end = p.L;
   if (p.lengths) {
     const int64_t n = p.lengths[seq];
@@ -48,78 +51,87 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(const ScanParam
   const int64_t first = (int64_t)(warp * TileT::kSubs + sub) * kSteps;
 
   float2 h = make_float2(0.0f, 0.0f);
-  if (p.h0) {
-    if (in0) h.x = p.h0[seq * p.d + c0];
-    if (in1) h.y = p.h0[seq * p.d + c0 + (kVec ? 1 : kLanes)];
-  }
+  if (p.h0) h = make_float2(p.h0[seq * p.d + c0], p.h0[seq * p.d + c0 + next]);
 
-  Pair<T> rv[kSteps], rg[kSteps], rz[kSteps];
-  auto fetch = [&](int64_t t0) {
-    const T* a = vp + t0 * p.v.rs;
-    const T* b = gp + t0 * p.g.rs;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const bool on = t0 + i < end;
-      rg[i] = load_pair<T, kVec, kLanes>(b + i * p.g.rs, on && in0, on && in1);
-      rv[i] = load_pair<T, kVec, kLanes>(a + i * p.v.rs, on && in0, on && in1);
-    }
-  };
-  auto fetch_z = [&](int64_t t0) {
-    const T* a = zp + t0 * p.z.rs;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const bool on = t0 + i < end;
-      rz[i] = load_pair<T, kVec, kLanes>(a + i * p.z.rs, on && in0, on && in1);
-    }
-  };
-
+  extern __shared__ __align__(16) uint8_t slots[];
+  using St = Stage<T, kGate ? 3 : 2>;
+  const St stage(slots);
   const int64_t rounds = (p.tiles + size - 1) / size;
-  fetch((int64_t)rank * TileT::kLen + first);
-  for (int64_t k = 0; k < rounds; ++k) {
+  auto fetch = [&](int64_t k) {
     const int64_t t0 = (k * size + rank) * TileT::kLen + first;
-    if constexpr (kGate) fetch_z(t0);
+    const int left = rows_left(end, t0), buf = (int)(k & 1);
+    stage.template fetch<kVec>(buf, 0, gp + t0 * p.g.rs, p.g.rs, next, left);
+    stage.template fetch<kVec>(buf, 1, vp + t0 * p.v.rs, p.v.rs, next, left);
+    if constexpr (kGate) stage.template fetch<kVec>(buf, 2, zp + t0 * p.z.rs, p.z.rs, next, left);
+    St::commit();
+  };
+  if (St::kBufs == 2 && rounds > 0) fetch(0);
+  for (int64_t k = 0; k < rounds; ++k) {
+    const int buf = (int)(k & 1);
+    if (St::kBufs == 1) {
+      fetch(k);
+      St::template wait<0>();
+    } else if (k + 1 < rounds) {
+      fetch(k + 1);
+      St::template wait<1>();
+    } else {
+      St::template wait<0>();
+    }
+    const int64_t t0 = (k * size + rank) * TileT::kLen + first;
     float2 f[kSteps], u[kSteps];
-    float4 m = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      const float2 g = pair_f32<T>(rg[i]), v = pair_f32<T>(rv[i]);
       float2 n;
-      gate_pair(g.x, f[i].x, n.x);
-      gate_pair(g.y, f[i].y, n.y);
-      u[i] = fmul2(n, v);
-      if (t0 + i >= end) {
-        f[i] = make_float2(1.0f, 1.0f);
-        u[i] = make_float2(0.0f, 0.0f);
-      }
-      const float2 a = fmul2(make_float2(m.x, m.y), f[i]);
-      const float2 b = ffma2(f[i], make_float2(m.z, m.w), u[i]);
-      m = make_float4(a.x, a.y, b.x, b.y);
+      gate2(stage.get(buf, 0, i), f[i], n);
+      u[i] = fmul2(n, stage.get(buf, 1, i));
     }
-    if (k + 1 < rounds) fetch(t0 + (int64_t)size * TileT::kLen);
-    float2 s = carry_in<kLanes, false>(sh, (int)(k & 1), m, h, rank, size);
+    if (end - t0 < kSteps) {  // steps behind the end leave the state
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+        if (i >= end - t0) {
+          f[i] = make_float2(1.0f, 1.0f);
+          u[i] = make_float2(0.0f, 0.0f);
+        }
+    }
+    float2 a = f[0], b = u[0];
+#pragma unroll
+    for (int i = 1; i < kSteps; ++i) {
+      a = fmul2(a, f[i]);
+      b = ffma2(f[i], b, u[i]);
+    }
+    float2 s = carry_in<kLanes, false>(sh, buf, make_float4(a.x, a.y, b.x, b.y), h, rank,
+                                       size);
     if (p.states && t0 < p.L && t0 % kGatedStateSteps == 0) {
       float* o = p.states + (seq * p.saved + t0 / kGatedStateSteps) * p.d + c0;
       if (in0) o[0] = s.x;
-      if (in1) o[kVec ? 1 : kLanes] = s.y;
+      if (in1) o[next] = s.y;
     }
     T* o = yp + t0 * p.y.rs;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
+    auto put = [&](int i) {
       s = ffma2(f[i], s, u[i]);
       float2 y = s;
       if constexpr (kGate) {
-        const float2 z = pair_f32<T>(rz[i]);
-        y = fmul2(s, make_float2(z.x * sigmoid_sfu(z.x), z.y * sigmoid_sfu(z.y)));
+        const float2 z = stage.get(buf, 2, i);
+        y = fmul2(s, fmul2(z, sigmoid2(z)));
       }
-      if (t0 + i >= end) y = make_float2(0.0f, 0.0f);
-      const bool on = t0 + i < p.L;
-      store_pair<T, kVec, kLanes>(o + i * p.y.rs, y, on && in0, on && in1);
+      return y;
+    };
+    if (t0 + kSteps <= end) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+        store_pair<T, kVec>(o + i * p.y.rs, next, put(i), in0, in1);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const float2 y = t0 + i < end ? put(i) : make_float2(0.0f, 0.0f);
+        if (t0 + i < p.L) store_pair<T, kVec>(o + i * p.y.rs, next, y, in0, in1);
+      }
     }
   }
   if (p.h_final && rank == 0 && warp == 0 && sub == 0) {
     float* o = p.h_final + seq * p.d + c0;
     if (in0) o[0] = h.x;
-    if (in1) o[kVec ? 1 : kLanes] = h.y;
+    if (in1) o[next] = h.y;
   }
 }
 
@@ -144,7 +156,8 @@ cudaError_t scan_type(const ssmq_gated_args& a, cudaStream_t st) {
   const bool vec = a.dim % 2 == 0 && pairs_ok<T>(a.v) && pairs_ok<T>(a.g) && pairs_ok<T>(a.z) &&
                    pairs_ok<T>(a.y);
   const bool z = a.z.p != nullptr;
-#define SSMQ_GATED(V, N, Z) return launch(gated_scan_kernel<T, V, N, Z>, p, s, st)
+#define SSMQ_GATED(V, N, Z) \
+  return launch<gated_scan_kernel<T, V, N, Z>>(p, s, Stage<T, Z ? 3 : 2>::kBytes, st)
   if (vec) {
     if (s.narrow) { if (z) SSMQ_GATED(true, 8, true); SSMQ_GATED(true, 8, false); }
     if (z) SSMQ_GATED(true, 32, true);
@@ -198,10 +211,10 @@ __global__ void __launch_bounds__(kUpdThreads) gated_update_kernel(const UpdateP
   float y[kN];
 #pragma unroll
   for (int j = 0; j < kN; ++j) {
-    float f, n;
-    gate_pair(g[j], f, n);
-    h[j] = fmaf(f, h[j], n * v[j]);
-    y[j] = zp ? h[j] * (z[j] * sigmoid_sfu(z[j])) : h[j];
+    float2 f, n;  // (the second half of the pair is not used)
+    gate2(make_float2(g[j], 0.0f), f, n);
+    h[j] = fmaf(f.x, h[j], n.x * v[j]);
+    y[j] = zp ? h[j] * (z[j] * sigmoid2(make_float2(z[j], 0.0f)).x) : h[j];
   }
   if constexpr (kVec) {
     store8(hp, pack8<float>(h));

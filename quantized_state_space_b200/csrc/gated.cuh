@@ -54,26 +54,22 @@ __device__ __forceinline__ float2 pair_f32(Pair<T> p) { return unpack2<T>(p.w); 
 template <>
 __device__ __forceinline__ float2 pair_f32<float>(Pair<float> p) { return p.w; }
 
-template <typename T, bool kVec, int kLanes>
-__device__ __forceinline__ Pair<T> load_pair(const T* p, bool in0, bool in1) {
+// Elements p[0] and p[next] (kVec: one load of a pair).
+template <typename T, bool kVec>
+__device__ __forceinline__ Pair<T> load_pair(const T* p, int next) {
   Pair<T> r;
   if constexpr (kVec) {
-    r = Pair<T>{};
-    if (in0) r = *reinterpret_cast<const Pair<T>*>(p);
+    r = *reinterpret_cast<const Pair<T>*>(p);
+  } else if constexpr (sizeof(T) == 4) {
+    r.w = make_float2(p[0], p[next]);
   } else {
-    if constexpr (sizeof(T) == 4) {
-      r.w.x = in0 ? p[0] : 0.0f;
-      r.w.y = in1 ? p[kLanes] : 0.0f;
-    } else {
-      const uint16_t* u = reinterpret_cast<const uint16_t*>(p);
-      const uint32_t a = in0 ? u[0] : 0u, b = in1 ? u[kLanes] : 0u;
-      r.w = a | (b << 16);
-    }
+    const uint16_t* u = reinterpret_cast<const uint16_t*>(p);
+    r.w = (uint32_t)u[0] | ((uint32_t)u[next] << 16);
   }
   return r;
 }
-template <typename T, bool kVec, int kLanes>
-__device__ __forceinline__ void store_pair(T* p, float2 v, bool in0, bool in1) {
+template <typename T, bool kVec>
+__device__ __forceinline__ void store_pair(T* p, int next, float2 v, bool in0, bool in1) {
   if constexpr (kVec) {
     if (in0) {
       if constexpr (sizeof(T) == 4)
@@ -83,21 +79,88 @@ __device__ __forceinline__ void store_pair(T* p, float2 v, bool in0, bool in1) {
     }
   } else {
     if (in0) p[0] = from_f32<T>(v.x);
-    if (in1) p[kLanes] = from_f32<T>(v.y);
+    if (in1) p[next] = from_f32<T>(v.y);
   }
 }
 
-// f = sigmoid(g), n = 1 - f = sigmoid(-g): the smaller one as e / (1 + e),
-// e = exp(-|g|), with full relative accuracy, the larger one as 1 - it.
-__device__ __forceinline__ void gate_pair(float g, float& f, float& n) {
-  const float e = ex2_sfu(-fabsf(g) * kLog2e);
-  const float s = e * rcp_sfu(1.0f + e);
-  const float l = 1.0f - s;
-  f = g >= 0.0f ? l : s;
-  n = g >= 0.0f ? s : l;
+// Staged inputs.  Every thread copies the pairs of its own steps into slots of
+// its own ([buffer][tensor][step][thread], conflict-free) one round ahead and
+// reads them back itself: no barrier, and no registers held by loads in flight.
+template <typename T, int kTensors>
+struct Stage {
+  // two buffers of 16-bit elements; binary32 has room for one
+  static constexpr int kBufs = sizeof(T) == 4 ? 1 : 2;
+  static constexpr int kPerBuf = kTensors * kSteps * kThreads;
+  static constexpr int kBytes = kBufs * kPerBuf * (int)sizeof(Pair<T>);
+  Pair<T>* mine;
+  __device__ __forceinline__ Stage(void* smem)
+      : mine(static_cast<Pair<T>*>(smem) + threadIdx.x) {}
+  __device__ __forceinline__ Pair<T>* at(int buf, int tensor) const {
+    return mine + (kBufs == 1 ? 0 : buf) * kPerBuf + tensor * kSteps * kThreads;
+  }
+  __device__ __forceinline__ float2 get(int buf, int tensor, int i) const {
+    return pair_f32<T>(at(buf, tensor)[i * kThreads]);
+  }
+  // rows 0 .. left - 1 of the thread's steps, zeros behind them.  Lanes without
+  // a channel have their pointers clamped to channel 0.
+  template <bool kVec>
+  __device__ __forceinline__ void fetch(int buf, int tensor, const T* p, int64_t rs, int next,
+                                        int left) const {
+    Pair<T>* o = at(buf, tensor);
+    if constexpr (kVec) {
+      const uint32_t dst = tc::smem_u32(o);
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int bytes = i < left ? (int)sizeof(Pair<T>) : 0;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(
+                         dst + i * kThreads * (int)sizeof(Pair<T>)),
+                     "l"(p + i * rs), "n"(sizeof(Pair<T>)), "r"(bytes)
+                     : "memory");
+      }
+    } else {
+      Pair<T> r[kSteps];
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        r[i] = Pair<T>{};
+        if (i < left) r[i] = load_pair<T, kVec>(p + i * rs, next);
+      }
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) o[i * kThreads] = r[i];
+    }
+  }
+  static __device__ __forceinline__ void commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  template <int kPending>
+  static __device__ __forceinline__ void wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+  }
+};
+// rows of the segment at t0 that lie before the end, at most kSteps
+__device__ __forceinline__ int rows_left(int64_t end, int64_t t0) {
+  const int64_t n = end - t0;
+  return n < 0 ? 0 : (n < kSteps ? (int)n : kSteps);
 }
-__device__ __forceinline__ float sigmoid_sfu(float z) {
-  return rcp_sfu(1.0f + ex2_sfu(-z * kLog2e));
+
+// e = exp(-g) with the exponent kept below 2^126, r = 1 / (1 + e): n = 1 - f =
+// e r and, for g < 0, f = r have full relative accuracy; for g >= 0, f is
+// formed as 1 - n (n <= 1/2: half an ulp), not as the approximate reciprocal,
+// whose ulp a long memory would accumulate.
+__device__ __forceinline__ void gate2(float2 g, float2& f, float2& n) {
+  const float2 x = fmul2(g, make_float2(-kLog2e, -kLog2e));
+  const float2 e = make_float2(ex2_sfu(fminf(x.x, 126.0f)), ex2_sfu(fminf(x.y, 126.0f)));
+  const float2 one = make_float2(1.0f, 1.0f);
+  const float2 d = fadd2(one, e);
+  const float2 r = make_float2(rcp_sfu(d.x), rcp_sfu(d.y));
+  n = fmul2(e, r);
+  const float2 c = fsub2(one, n);
+  f.x = g.x < 0.0f ? r.x : c.x;
+  f.y = g.y < 0.0f ? r.y : c.y;
+}
+__device__ __forceinline__ float2 sigmoid2(float2 z) {
+  const float2 x = fmul2(z, make_float2(-kLog2e, -kLog2e));
+  const float2 d = fadd2(make_float2(1.0f, 1.0f), make_float2(ex2_sfu(x.x), ex2_sfu(x.y)));
+  return make_float2(rcp_sfu(d.x), rcp_sfu(d.y));
 }
 
 // ---- cluster ---------------------------------------------------------------
@@ -126,11 +189,13 @@ __device__ __forceinline__ void push_f4(float4* local, uint32_t rank, float4 v) 
 
 // (A, B) of two channels: {A0, A1, B0, B1}; h -> A h + B
 __device__ __forceinline__ float2 apply(float4 m, float2 h) {
-  return make_float2(fmaf(m.x, h.x, m.z), fmaf(m.y, h.y, m.w));
+  return ffma2(make_float2(m.x, m.y), h, make_float2(m.z, m.w));
 }
 // first m, then n
 __device__ __forceinline__ float4 compose(float4 m, float4 n) {
-  return make_float4(m.x * n.x, m.y * n.y, fmaf(n.x, m.z, n.z), fmaf(n.y, m.w, n.w));
+  const float2 a = fmul2(make_float2(m.x, m.y), make_float2(n.x, n.y));
+  const float2 b = apply(n, make_float2(m.z, m.w));
+  return make_float4(a.x, a.y, b.x, b.y);
 }
 __device__ __forceinline__ float4 shfl_f4(float4 v, int src) {
   return make_float4(__shfl_sync(0xFFFFFFFFu, v.x, src), __shfl_sync(0xFFFFFFFFu, v.y, src),
@@ -170,12 +235,12 @@ __device__ __forceinline__ float2 carry_in(Shared<kLanes>& sh, int buf, float4 m
     if (sub > 0) mine = before;
   }
   __syncthreads();
-  float4 pre = make_float4(1.0f, 1.0f, 0.0f, 0.0f), all = pre;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    if (i == w) pre = all;
-    all = compose(all, sh.warp[buf][i][l]);
-  }
+  float4 pre = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+#pragma unroll 1
+  for (int i = 0; i < w; ++i) pre = compose(pre, sh.warp[buf][i][l]);
+  float4 all = pre;
+#pragma unroll 1
+  for (int i = w; i < kWarps; ++i) all = compose(all, sh.warp[buf][i][l]);
   float2 base = h;
   if (size > 1) {
     // warp i tells CTA i of the cluster what this CTA's tile does to a state
@@ -202,9 +267,9 @@ struct Shape {
 };
 inline Shape shape_for(int64_t b, int64_t L, int64_t d) {
   Shape s;
-  // Enough CTAs for two per SM, first by splitting time over a cluster, then
+  // Enough CTAs for eight per SM, first by splitting time over a cluster, then
   // by narrower channel blocks (32-byte rows of 16-bit elements).
-  const int64_t want = 2 * (int64_t)sm_count();
+  const int64_t want = 8 * (int64_t)sm_count();
   auto pick = [&](int channels, int len) {
     s.blocks = (d + channels - 1) / channels;
     const int64_t tiles = (L + len - 1) / len;
@@ -215,7 +280,7 @@ inline Shape shape_for(int64_t b, int64_t L, int64_t d) {
   };
   s.narrow = false;
   int64_t n = pick(Tile<32>::kChannels, Tile<32>::kLen);
-  if (n < want) {
+  if (n < want / 4) {
     const Shape wide = s;
     s.narrow = true;
     const int64_t m = pick(Tile<8>::kChannels, Tile<8>::kLen);
@@ -226,11 +291,15 @@ inline Shape shape_for(int64_t b, int64_t L, int64_t d) {
   return s;
 }
 
-template <typename Kernel, typename Params>
-cudaError_t launch(Kernel kern, const Params& p, const Shape& s, cudaStream_t st) {
+template <auto kern, typename Params>
+cudaError_t launch(const Params& p, const Shape& s, int smem, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, done);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(s.grid);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;

@@ -8,8 +8,8 @@
 // the c behind it to the c in front of it as c -> A c + R with the A of its
 // forward map.
 //
-// Bound: HBM (v, g, z, dy in, dv, dg, dz out).  A tile's steps stay in
-// registers: the forward states inside it are rebuilt from the state that the
+// Bound: HBM (v, g, z, dy in, dv, dg, dz out).  A tile's gates stay in
+// registers and its inputs in shared memory (copied one round ahead): the forward states inside it are rebuilt from the state that the
 // forward call saved at its start (one per 64 steps), so neither h nor the
 // gates cross memory, and only c travels between the CTAs of a cluster.
 #include "gated.cuh"
@@ -39,9 +39,10 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_grad_kernel(const Grad
   const int64_t seq = unit / p.blocks, blk = unit % p.blocks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / kLanes, l = lane % kLanes;
-  const int64_t c0 = blk * TileT::kChannels + (kVec ? 2 * l : l);
-  constexpr int kNext = kVec ? 1 : kLanes;
-  const bool in0 = c0 < p.d, in1 = c0 + kNext < p.d;
+  int64_t c0 = blk * TileT::kChannels + (kVec ? 2 * l : l);
+  const bool in0 = c0 < p.d, in1 = c0 + (kVec ? 1 : kLanes) < p.d;
+  const int next = kVec ? 1 : (in1 ? kLanes : 0);
+  if (!in0) c0 = 0;
   int64_t end = p.L;
   if (p.lengths) {
     const int64_t n = p.lengths[seq];
@@ -57,60 +58,78 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_grad_kernel(const Grad
   const int first = (warp * TileT::kSubs + sub) * kSteps;
 
   float2 c = make_float2(0.0f, 0.0f);
-  if (p.dh_final) {
-    if (in0) c.x = p.dh_final[seq * p.d + c0];
-    if (in1) c.y = p.dh_final[seq * p.d + c0 + kNext];
-  }
+  if (p.dh_final)
+    c = make_float2(p.dh_final[seq * p.d + c0], p.dh_final[seq * p.d + c0 + next]);
 
+  extern __shared__ __align__(16) uint8_t slots[];
+  using St = Stage<T, kGate ? 4 : 3>;
+  const St stage(slots);
   const int64_t rounds = (p.tiles + size - 1) / size;
+  // tiles from the last one backwards; rank 0 holds the latest of a round
+  auto tile_of = [&](int64_t k) { return p.tiles - 1 - (k * size + rank); };
+  auto fetch = [&](int64_t k) {
+    const int64_t tile = tile_of(k);
+    const int64_t t0 = tile >= 0 ? tile * TileT::kLen + first : 0;
+    const int left = tile >= 0 ? rows_left(end, t0) : 0, buf = (int)(k & 1);
+    stage.template fetch<kVec>(buf, 0, gp + t0 * p.g.rs, p.g.rs, next, left);
+    stage.template fetch<kVec>(buf, 1, vp + t0 * p.v.rs, p.v.rs, next, left);
+    stage.template fetch<kVec>(buf, 2, dyp + t0 * p.dy.rs, p.dy.rs, next, left);
+    if constexpr (kGate) stage.template fetch<kVec>(buf, 3, zp + t0 * p.z.rs, p.z.rs, next, left);
+    St::commit();
+  };
+  if (St::kBufs == 2 && rounds > 0) fetch(0);
   for (int64_t k = 0; k < rounds; ++k) {
-    // tiles from the last one backwards; rank 0 holds the latest of a round
-    const int64_t tile = p.tiles - 1 - (k * size + rank);
-    const int64_t t0 = tile * TileT::kLen + first;
-    const bool real = tile >= 0;
-    Pair<T> rv[kSteps], rg[kSteps], rz[kSteps], rd[kSteps];
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const bool on = real && t0 + i < end;
-      const int64_t t = t0 + i;
-      rg[i] = load_pair<T, kVec, kLanes>(gp + t * p.g.rs, on && in0, on && in1);
-      rv[i] = load_pair<T, kVec, kLanes>(vp + t * p.v.rs, on && in0, on && in1);
-      rd[i] = load_pair<T, kVec, kLanes>(dyp + t * p.dy.rs, on && in0, on && in1);
-      if constexpr (kGate)
-        rz[i] = load_pair<T, kVec, kLanes>(zp + t * p.z.rs, on && in0, on && in1);
+    const int buf = (int)(k & 1);
+    if (St::kBufs == 1) {
+      fetch(k);
+      St::template wait<0>();
+    } else if (k + 1 < rounds) {
+      fetch(k + 1);
+      St::template wait<1>();
+    } else {
+      St::template wait<0>();
     }
+    const int64_t tile = tile_of(k);
+    const bool real = tile >= 0;
+    const int64_t t0 = real ? tile * TileT::kLen + first : 0;
+    const int left = real ? rows_left(end, t0) : 0;
     float2 hs = make_float2(0.0f, 0.0f);  // state before the tile
     if (real) {
       const float* sp = p.states +
                         (seq * p.saved + tile * (TileT::kLen / kGatedStateSteps)) * p.d + c0;
-      if (in0) hs.x = sp[0];
-      if (in1) hs.y = sp[kNext];
+      hs = make_float2(sp[0], sp[next]);
     }
 
-    float2 f[kSteps], n[kSteps], dh[kSteps];
-    float2 a = make_float2(1.0f, 1.0f), b = make_float2(0.0f, 0.0f), r = b;
+    // f and n of a step; f = 1, n = 0 behind the end
+    float2 f[kSteps], n[kSteps], sg[kSteps];
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      const float2 g = pair_f32<T>(rg[i]);
-      gate_pair(g.x, f[i].x, n[i].x);
-      gate_pair(g.y, f[i].y, n[i].y);
-      if (!real || t0 + i >= end) {
-        f[i] = make_float2(1.0f, 1.0f);
-        n[i] = make_float2(0.0f, 0.0f);
-      }
+      gate2(stage.get(buf, 0, i), f[i], n[i]);
+      if constexpr (kGate) sg[i] = sigmoid2(stage.get(buf, 3, i));
+    }
+    if (left < kSteps) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+        if (i >= left) {
+          f[i] = make_float2(1.0f, 1.0f);
+          n[i] = make_float2(0.0f, 0.0f);
+        }
+    }
+    auto dh = [&](int i) {  // dy silu(z)
+      const float2 d = stage.get(buf, 2, i);
+      if constexpr (kGate) return fmul2(d, fmul2(stage.get(buf, 3, i), sg[i]));
+      return d;
+    };
+    float2 a = f[0], b = fmul2(n[0], stage.get(buf, 1, 0)), r = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 1; i < kSteps; ++i) {
       a = fmul2(a, f[i]);
-      b = ffma2(f[i], b, fmul2(n[i], pair_f32<T>(rv[i])));
-      dh[i] = pair_f32<T>(rd[i]);
-      if constexpr (kGate) {
-        const float2 z = pair_f32<T>(rz[i]);
-        dh[i] = fmul2(dh[i], make_float2(z.x * sigmoid_sfu(z.x), z.y * sigmoid_sfu(z.y)));
-      }
+      b = ffma2(f[i], b, fmul2(n[i], stage.get(buf, 1, i)));
     }
 #pragma unroll
-    for (int i = kSteps - 1; i >= 0; --i) r = fmul2(f[i], fadd2(dh[i], r));
+    for (int i = kSteps - 1; i >= 0; --i) r = fmul2(f[i], fadd2(dh(i), r));
 
     // forward state before this thread's segment: maps of the CTA's earlier segments
-    const int buf = (int)(k & 1);
     {
       float4 m = make_float4(a.x, a.y, b.x, b.y);
       constexpr int kSubs = TileT::kSubs;
@@ -126,48 +145,54 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_grad_kernel(const Grad
         if (sub > 0) mine = before;
       }
       // (the barrier inside carry_in orders s_fwd as well)
-      const float2 cin = carry_in<kLanes, true>(sh, buf, make_float4(a.x, a.y, r.x, r.y), c, rank,
-                                                size);
+      r = carry_in<kLanes, true>(sh, buf, make_float4(a.x, a.y, r.x, r.y), c, rank, size);
+#pragma unroll 1
       for (int w = 0; w < warp; ++w) hs = apply(s_fwd[buf][w][l], hs);
       hs = apply(mine, hs);
-      r = cin;
     }
 
     float2 hb[kSteps];  // h_{t-1}
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       hb[i] = hs;
-      hs = ffma2(f[i], hs, fmul2(n[i], pair_f32<T>(rv[i])));
+      hs = ffma2(f[i], hs, fmul2(n[i], stage.get(buf, 1, i)));
     }
-    if (real) {
-#pragma unroll
-      for (int i = kSteps - 1; i >= 0; --i) {
-        const int64_t t = t0 + i;
-        const bool on = t < p.L;
-        const float2 lam = fadd2(dh[i], r);
-        float2 dv = fmul2(n[i], lam);
-        r = fmul2(f[i], lam);
-        float2 dg = fmul2(dv, fmul2(f[i], fsub2(hb[i], pair_f32<T>(rv[i]))));
-        if (t >= end) dv = dg = make_float2(0.0f, 0.0f);
-        store_pair<T, kVec, kLanes>(dvp + t * p.dv.rs, dv, on && in0, on && in1);
-        store_pair<T, kVec, kLanes>(dgp + t * p.dg.rs, dg, on && in0, on && in1);
-        if constexpr (kGate) {
-          const float2 z = pair_f32<T>(rz[i]);
-          const float2 d = pair_f32<T>(rd[i]);
-          const float2 h = i + 1 < kSteps ? hb[i + 1 < kSteps ? i + 1 : i] : hs;
-          const float sx = sigmoid_sfu(z.x), sy = sigmoid_sfu(z.y);
-          float2 dz = make_float2(d.x * h.x * (sx * fmaf(z.x, 1.0f - sx, 1.0f)),
-                                  d.y * h.y * (sy * fmaf(z.y, 1.0f - sy, 1.0f)));
-          if (t >= end) dz = make_float2(0.0f, 0.0f);
-          store_pair<T, kVec, kLanes>(dzp + t * p.dz.rs, dz, on && in0, on && in1);
-        }
+    T* dvo = dvp + t0 * p.dv.rs;
+    T* dgo = dgp + t0 * p.dg.rs;
+    T* dzo = kGate ? dzp + t0 * p.dz.rs : nullptr;
+    // gradients of step i, from the last step backwards
+    auto put = [&](int i, bool live, bool row) {
+      const float2 lam = fadd2(dh(i), r);
+      r = fmul2(f[i], lam);
+      float2 dv = fmul2(n[i], lam);
+      float2 dg = fmul2(dv, fmul2(f[i], fsub2(hb[i], stage.get(buf, 1, i))));
+      if (!live) dv = dg = make_float2(0.0f, 0.0f);
+      if (row) {
+        store_pair<T, kVec>(dvo + i * p.dv.rs, next, dv, in0, in1);
+        store_pair<T, kVec>(dgo + i * p.dg.rs, next, dg, in0, in1);
       }
+      if constexpr (kGate) {
+        // silu'(z) = s (1 + z (1 - s))
+        const float2 z = stage.get(buf, 3, i), one = make_float2(1.0f, 1.0f);
+        const float2 h = i + 1 < kSteps ? hb[i + 1 < kSteps ? i + 1 : i] : hs;
+        const float2 ds = fmul2(sg[i], ffma2(z, fsub2(one, sg[i]), one));
+        float2 dz = fmul2(fmul2(stage.get(buf, 2, i), h), ds);
+        if (!live) dz = make_float2(0.0f, 0.0f);
+        if (row) store_pair<T, kVec>(dzo + i * p.dz.rs, next, dz, in0, in1);
+      }
+    };
+    if (left >= kSteps) {
+#pragma unroll
+      for (int i = kSteps - 1; i >= 0; --i) put(i, true, true);
+    } else if (real) {
+#pragma unroll
+      for (int i = kSteps - 1; i >= 0; --i) put(i, i < left, t0 + i < p.L);
     }
   }
   if (p.dh0 && rank == 0 && warp == 0 && sub == 0) {
     float* o = p.dh0 + seq * p.d + c0;
     if (in0) o[0] = c.x;
-    if (in1) o[kNext] = c.y;
+    if (in1) o[next] = c.y;
   }
 }
 
@@ -196,7 +221,8 @@ cudaError_t grad_type(const ssmq_gated_grad_args& a, cudaStream_t st) {
   const bool vec = a.dim % 2 == 0 && pairs_ok<T>(a.v) && pairs_ok<T>(a.g) && pairs_ok<T>(a.dy) &&
                    pairs_ok<T>(a.dv) && pairs_ok<T>(a.dg) &&
                    (!z || (pairs_ok<T>(a.z) && pairs_ok<T>(a.dz)));
-#define SSMQ_GATED(V, N, Z) return launch(gated_scan_grad_kernel<T, V, N, Z>, p, s, st)
+#define SSMQ_GATED(V, N, Z) \
+  return launch<gated_scan_grad_kernel<T, V, N, Z>>(p, s, Stage<T, Z ? 4 : 3>::kBytes, st)
   if (vec) {
     if (s.narrow) { if (z) SSMQ_GATED(true, 8, true); SSMQ_GATED(true, 8, false); }
     if (z) SSMQ_GATED(true, 32, true);

@@ -586,9 +586,9 @@ cudaError_t launch_split(const CUtensorMap& wmap, const CUtensorMap& xmap, LinPa
     while (split < kMaxSplit && tiles * split * 2 <= sm_count() && p.kblocks >= 8 * split)
       split *= 2;
   static_assert(Cfg::kSmem <= 227 * 1024, "shared memory");
-  const cudaError_t e =
-      cudaFuncSetAttribute(int8_linear_split_kernel<kTok>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(int8_linear_split_kernel<kTok>),
+                                   Cfg::kSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * split));
@@ -673,8 +673,8 @@ cudaError_t launch_int8_linear(const ssmq_linear_args& a, void* ws, cudaStream_t
   p.tok_tiles = (p.M + kPairTok - 1) / kPairTok;
   p.ch_tiles = (p.N + kPairCh - 1) / kPairCh;
   p.group = 16;
-  e = cudaFuncSetAttribute(int8_linear_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kPairSmem);
+  static std::atomic<uint64_t> done{0};
+  e = allow_smem(reinterpret_cast<const void*>(int8_linear_pair_kernel), kPairSmem, done);
   if (e != cudaSuccess) return e;
   const int64_t pairs = pair_tiles < sms / 2 ? pair_tiles : sms / 2;
   int8_linear_pair_kernel<<<(unsigned)(2 * pairs), kPairThreads, kPairSmem, st>>>(wmap, xmap, p);
