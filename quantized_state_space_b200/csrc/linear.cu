@@ -119,17 +119,45 @@ __device__ __forceinline__ void arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
 }
-// 16 columns of this thread's TMEM lane, complete when the statement ends
-__device__ __forceinline__ void tmem_ld16i(uint32_t taddr, int (&v)[16]) {
+// 32 (16) columns of this thread's TMEM lane; usable after tmem_done, through
+// which the registers pass so that no use moves in front of the wait
+__device__ __forceinline__ void tmem_get(uint32_t taddr, int (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
+        "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
+        "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_get(uint32_t taddr, int (&v)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      "%12, %13, %14, %15}, [%16];"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
         "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
         "=r"(v[14]), "=r"(v[15])
       : "r"(taddr)
       : "memory");
+}
+__device__ __forceinline__ void tmem_done(int (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]),
+                 "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                 "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                 "+r"(v[30]), "+r"(v[31])::"memory");
+}
+__device__ __forceinline__ void tmem_done(int (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])::"memory");
 }
 
 // ---- epilogue: one lane's channel, consecutive tokens --------------------------
@@ -146,27 +174,53 @@ __device__ __forceinline__ Channel channel_of(const LinParams& p, int64_t n) {
   c.bias = c.in && p.bias ? __ldg(p.bias + n) : 0.0f;
   return c;
 }
-template <typename T>
-__device__ __forceinline__ void store_one(const LinParams& p, const Channel& c, int64_t t, int acc) {
-  if (t < p.M && c.in) {
-    const float v = fmaf((float)acc, __ldg(p.xs + t) * c.scale, c.bias);
-    static_cast<T*>(p.y)[t * p.ldy + c.n] = from_f32<T>(v);
+// the scale of token t0 + lane, which the other lanes read by shuffle
+__device__ __forceinline__ float token_scale(const LinParams& p, int64_t t0, int n) {
+  const int lane = threadIdx.x & 31;
+  return lane < n && t0 + lane < p.M ? __ldg(p.xs + t0 + lane) : 0.0f;
+}
+// kN tokens from t0; xs holds the scale of token t0 + at in lane `at`
+template <typename T, int kN>
+__device__ __forceinline__ void store_tokens(const LinParams& p, const Channel& c, int64_t t0,
+                                             float xs, const int (&acc)[kN]) {
+  T* y = static_cast<T*>(p.y) + t0 * p.ldy + c.n;
+  const int64_t left = p.M - t0;  // (the same in the whole warp)
+  if (left >= kN) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const float s = __shfl_sync(0xFFFFFFFFu, xs, i);
+      if (c.in) y[0] = from_f32<T>(fmaf((float)acc[i], s * c.scale, c.bias));
+      y += p.ldy;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const float s = __shfl_sync(0xFFFFFFFFu, xs, i);
+      if (c.in && i < left) y[0] = from_f32<T>(fmaf((float)acc[i], s * c.scale, c.bias));
+      y += p.ldy;
+    }
   }
 }
-template <typename T>
-__device__ __forceinline__ void store16(const LinParams& p, const Channel& c, int64_t t0,
-                                        const int (&acc)[16]) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) store_one<T>(p, c, t0 + i, acc[i]);
-}
-__device__ __forceinline__ void store16_any(const LinParams& p, const Channel& c, int64_t t0,
-                                            const int (&acc)[16]) {
+template <int kN>
+__device__ __forceinline__ void store_any(const LinParams& p, const Channel& c, int64_t t0,
+                                          float xs, const int (&acc)[kN]) {
   if (p.dtype == SSMQ_F16)
-    store16<__half>(p, c, t0, acc);
+    store_tokens<__half>(p, c, t0, xs, acc);
   else if (p.dtype == SSMQ_BF16)
-    store16<__nv_bfloat16>(p, c, t0, acc);
+    store_tokens<__nv_bfloat16>(p, c, t0, xs, acc);
   else
-    store16<float>(p, c, t0, acc);
+    store_tokens<float>(p, c, t0, xs, acc);
+}
+__device__ __forceinline__ void store_one(const LinParams& p, const Channel& c, int64_t t, float xs,
+                                          int acc) {
+  if (!c.in) return;
+  const float v = fmaf((float)acc, xs * c.scale, c.bias);
+  if (p.dtype == SSMQ_F16)
+    static_cast<__half*>(p.y)[t * p.ldy + c.n] = __float2half_rn(v);
+  else if (p.dtype == SSMQ_BF16)
+    static_cast<__nv_bfloat16*>(p.y)[t * p.ldy + c.n] = __float2bfloat16_rn(v);
+  else
+    static_cast<float*>(p.y)[t * p.ldy + c.n] = v;
 }
 
 // ---- few tokens: 128 channels x kTok tokens per cluster, K split over its CTAs --
@@ -181,28 +235,31 @@ constexpr int kMaxSplit = 8;
 template <int kTok>
 struct SplitCfg {
   static constexpr int kStage = kOperand + kTok * kBlockK;
-  static constexpr int kRed = kTok <= 128 ? kTok * kRows * 4 : 0;
-  // two CTAs per SM up to 64 tokens, so that a cluster finds its SMs easily
-  static constexpr int kBudget = (kTok <= 64 ? 108 : 216) * 1024;
-  static constexpr int kStages = (kBudget - kRed) / kStage;
-  static constexpr int kSmem = 1024 + kStages * kStage + kRed + 256;
+  static constexpr int kRed = kTok * kRows * 4;  // with a split only
+  static constexpr int kBars = 256;              // barriers, TMEM address, abort word
+  static constexpr int kMaxStages = 12;
   static constexpr int kCols = kTok < 32 ? 32 : kTok;
+  static constexpr int kLd = kTok < 32 ? 16 : 32;  // token columns per TMEM load
+  static int smem(int stages, bool split) {
+    return 1024 + kBars + stages * kStage + (split ? kRed : 0);
+  }
 };
 
 template <int kTok>
 __global__ void __launch_bounds__(kSplitThreads)
     int8_linear_split_kernel(const __grid_constant__ CUtensorMap wmap,
                              const __grid_constant__ CUtensorMap xmap, const LinParams p,
-                             const int split) {
+                             const int split, const int stages) {
   using Cfg = SplitCfg<kTok>;
+  constexpr int kLd = Cfg::kLd;
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~1023ull);
-  int* red = reinterpret_cast<int*>(base + Cfg::kStages * Cfg::kStage);
-  uint64_t* full = reinterpret_cast<uint64_t*>(base + Cfg::kStages * Cfg::kStage + Cfg::kRed);
-  uint64_t* empty = full + Cfg::kStages;
-  uint64_t* done = empty + Cfg::kStages;
+  uint64_t* full = reinterpret_cast<uint64_t*>(base + stages * Cfg::kStage);
+  uint64_t* empty = full + Cfg::kMaxStages;
+  uint64_t* done = empty + Cfg::kMaxStages;
   uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile uint32_t* gave_up = slot + 1;
+  int* red = reinterpret_cast<int*>(base + stages * Cfg::kStage + Cfg::kBars);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = split > 1 ? cta_rank() : 0;
@@ -211,13 +268,25 @@ __global__ void __launch_bounds__(kSplitThreads)
   const int kb0 = (int)((int64_t)p.kblocks * rank / split);
   const int kb1 = (int)((int64_t)p.kblocks * (rank + 1) / split);
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < Cfg::kStages; ++i) {
+  auto load = [&](int kb, int s) {
+    const uint32_t bar = tc::smem_u32(full + s);
+    const uint32_t dst = tc::smem_u32(base + s * Cfg::kStage);
+    stream::expect_tx(full + s, Cfg::kStage);
+    tma_load(dst, &wmap, kb * kBlockK, (int)ch0, bar);
+    tma_load(dst + kOperand, &xmap, kb * kBlockK, (int)tok0, bar);
+  };
+  const int first = kb1 - kb0 < stages ? kb1 - kb0 : stages;  // loads without a wait
+  if (warp == 4 && lane == 0) {
+    prefetch_map(&wmap);
+    prefetch_map(&xmap);
+    for (int i = 0; i < stages; ++i) {
       tc::mbar_init(full + i, 1);
       tc::mbar_init(empty + i, 1);
     }
     tc::mbar_init(done, 1);
     *gave_up = 0;
+    // the copies that need no empty stage start before the CTA meets
+    for (int i = 0; i < first; ++i) load(kb0 + i, i);
   }
   if (warp == 5) tc::tmem_alloc(slot, Cfg::kCols);
   tc::fence_before();
@@ -227,32 +296,28 @@ __global__ void __launch_bounds__(kSplitThreads)
   const uint32_t tmem = *slot;
 
   if (warp == 4 && lane == 0) {
-    prefetch_map(&wmap);
-    prefetch_map(&xmap);
-    int i = 0;
-    for (int kb = kb0; kb < kb1; ++kb, ++i) {
-      const int s = i % Cfg::kStages;
-      if (i >= Cfg::kStages &&
-          !tc::mbar_wait(empty + s, (uint32_t)(i / Cfg::kStages - 1) & 1u, kWaitLimit)) {
+    int s = 0;
+    uint32_t phase = 0;
+    int kb = kb0 + first;
+    for (; kb < kb1; ++kb) {
+      if (!tc::mbar_wait(empty + s, phase, kWaitLimit)) {
         *gave_up = 1;
         break;
       }
-      const uint32_t bar = tc::smem_u32(full + s);
-      const uint32_t dst = tc::smem_u32(base + s * Cfg::kStage);
-      stream::expect_tx(full + s, Cfg::kStage);
-      tma_load(dst, &wmap, kb * kBlockK, (int)ch0, bar);
-      tma_load(dst + kOperand, &xmap, kb * kBlockK, (int)tok0, bar);
+      load(kb, s);
+      if (++s == stages) s = 0, phase ^= 1u;
     }
     if (*gave_up) {  // copies in flight land before the CTA leaves
-      for (int j = i > Cfg::kStages ? i - Cfg::kStages : 0; j < i; ++j)
-        tc::mbar_wait(full + j % Cfg::kStages, (uint32_t)(j / Cfg::kStages) & 1u, kWaitLimit);
+      const int n = kb - kb0;  // copies issued
+      for (int j = n > stages ? n - stages : 0; j < n; ++j)
+        tc::mbar_wait(full + j % stages, (uint32_t)(j / stages) & 1u, kWaitLimit);
     }
   } else if (warp == 5 && lane == 0) {
     constexpr uint32_t idesc = idesc_i8(kRows, kTok);
-    int i = 0;
-    for (int kb = kb0; kb < kb1; ++kb, ++i) {
-      const int s = i % Cfg::kStages;
-      if (!tc::mbar_wait(full + s, (uint32_t)(i / Cfg::kStages) & 1u, kWaitLimit)) {
+    int s = 0;
+    uint32_t phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!tc::mbar_wait(full + s, phase, kWaitLimit)) {
         *gave_up = 1;
         break;
       }
@@ -261,60 +326,63 @@ __global__ void __launch_bounds__(kSplitThreads)
       const uint64_t ad = sw128_desc(a), bd = sw128_desc(a + kOperand);
 #pragma unroll
       for (int q = 0; q < kBlockK / 32; ++q)
-        mma_i8<1>(tmem, ad + 2 * q, bd + 2 * q, idesc, i > 0 || q > 0);
+        mma_i8<1>(tmem, ad + 2 * q, bd + 2 * q, idesc, kb > kb0 || q > 0);
       tc::mma_commit(empty + s);
+      if (++s == stages) s = 0, phase ^= 1u;
     }
     tc::mma_commit(done);
   }
   __syncwarp();
 
-  const Channel c = channel_of(p, ch0 + (warp & 3) * 32 + lane);
+  const int per = (kTok + split - 1) / split;  // token columns that a CTA finishes
+  const int ch = (warp & 3) * 32 + lane;
   const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+  Channel c;
   if (warp < 4) {
+    c = channel_of(p, ch0 + ch);
+    float xs = split == 1 ? token_scale(p, tok0, kLd) : 0.0f;
     if (!tc::mbar_wait(done, 0, kWaitLimit)) *gave_up = 1;
+    __syncwarp();
     tc::fence_after();
-    if (split == 1) {
-      for (int j = 0; j < kTok; j += 16) {
-        int v[16];
-        tmem_ld16i(lanes + j, v);
-        if (tok0 + j < p.M) store16_any(p, c, tok0 + j, v);
+    for (int j = 0; j < kTok; j += kLd) {
+      if (tok0 + j >= p.M) break;
+      int v[kLd];
+      tmem_get(lanes + j, v);
+      tmem_done(v);
+      if (split == 1) {
+        const float next = token_scale(p, tok0 + j + kLd, kLd);
+        store_any(p, c, tok0 + j, xs, v);
+        xs = next;
+      } else {
+        // column j goes to CTA j / per, which keeps [part][column][channel]
+        int owner = j / per, at = j % per;
+        const uint32_t local = tc::smem_u32(red + (int)rank * per * kRows + ch);
+#pragma unroll
+        for (int i = 0; i < kLd; ++i) {
+          asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(
+                           mapa(local + (uint32_t)at * kRows * 4, (uint32_t)owner)),
+                       "r"(v[i])
+                       : "memory");
+          if (++at == per) at = 0, ++owner;
+        }
       }
     }
   }
-  if constexpr (Cfg::kRed > 0) {
-    if (split > 1) {
-      // column j goes to CTA j / per, which keeps [part][column][channel]
-      const int per = (kTok + split - 1) / split;
-      const int ch = (warp & 3) * 32 + lane;
-      if (warp < 4) {
-        for (int j = 0; j < kTok; j += 16) {
-          if (tok0 + j >= p.M) break;
-          int v[16];
-          tmem_ld16i(lanes + j, v);
-          int owner = j / per, at = j % per;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint32_t dst = mapa(
-                tc::smem_u32(red + ((int)rank * per + at) * kRows + ch), (uint32_t)owner);
-            asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(dst), "r"(v[i]) : "memory");
-            if (++at == per) at = 0, ++owner;
-          }
-        }
-      }
-      cluster_sync();
-      if (warp < 4) {
-        for (int j = 0; j < per; ++j) {
-          const int64_t t = tok0 + (int64_t)rank * per + j;
-          if ((int)rank * per + j >= kTok || t >= p.M) break;
-          int acc = 0;
-          for (int r = 0; r < split; ++r) acc += red[(r * per + j) * kRows + ch];
-          if (p.dtype == SSMQ_F16)
-            store_one<__half>(p, c, t, acc);
-          else if (p.dtype == SSMQ_BF16)
-            store_one<__nv_bfloat16>(p, c, t, acc);
-          else
-            store_one<float>(p, c, t, acc);
-        }
+  if (split > 1) {
+    // this CTA's columns: their scales arrive while the others finish
+    const int64_t mine = tok0 + (int64_t)rank * per;
+    const int64_t left = p.M - mine;
+    int n = kTok - (int)rank * per;
+    n = n < per ? n : per;
+    n = left < n ? (int)left : n;
+    const float xs = warp < 4 ? token_scale(p, mine, per) : 0.0f;
+    cluster_sync();
+    if (warp < 4) {
+      for (int j = 0; j < n; ++j) {
+        int acc = 0;
+        for (int r = 0; r < split; ++r) acc += red[(r * per + j) * kRows + ch];
+        const float s = per <= 32 ? __shfl_sync(0xFFFFFFFFu, xs, j & 31) : __ldg(p.xs + mine + j);
+        store_one(p, c, mine + j, s, acc);
       }
     }
   }
@@ -329,8 +397,9 @@ __global__ void __launch_bounds__(kSplitThreads)
 // each brings 128 channels and 128 tokens per K block (half the operand
 // traffic per MMA of two separate 128 x 256 tiles), the leader issues the
 // MMAs of both.  Accumulators are double-buffered in TMEM (2 x 256 columns),
-// so four warps per CTA write tile i while the MMAs of tile i + 1 run.
-constexpr int kPairThreads = 256;  // warp 0 TMA, 1 MMA, 2 TMEM, 4-7 epilogue
+// so eight warps per CTA write tile i while the MMAs of tile i + 1 run (four were
+// slower than the MMAs: 206 against 126 us of MMAs at 16384 x 2560 x 5120).
+constexpr int kPairThreads = 384;  // warp 0 TMA, 1 MMA, 2 TMEM, 4-11 epilogue
 constexpr int kPairStages = 6;
 constexpr int kPairStage = 2 * kOperand;
 constexpr int kPairTok = 256, kPairCh = 256;
@@ -372,7 +441,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(acc_full + i, 1);
-      tc::mbar_init(acc_empty + i, 2 * 4);  // the epilogue warps of both CTAs
+      tc::mbar_init(acc_empty + i, 2 * 8);  // the epilogue warps of both CTAs
     }
     *gave_up = 0;
   }
@@ -448,27 +517,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
     }
     if (!ok) *gave_up = 1;
   } else if (warp >= 4) {
-    const int quarter = warp & 3;
+    const int quarter = warp & 3;                  // TMEM lanes that the warp may read
+    const int half = (warp - 4) / 4 * (kPairTok / 2);  // its token columns
     int64_t n = 0;
     for (int64_t t = pair; t < tiles; t += pairs, ++n) {
       const int b = (int)(n & 1);
       int64_t ch, tok;
       tile_at(p, t, ch, tok);
       const Channel c = channel_of(p, ch * kPairCh + rank * kRows + quarter * 32 + lane);
-      if (!tc::mbar_wait(acc_full + b, (uint32_t)(n / 2) & 1u, kWaitLimit)) {
+      const int64_t t0 = tok * kPairTok + half;
+      float xs[kPairTok / 64];
+#pragma unroll
+      for (int q = 0; q < kPairTok / 64; ++q) xs[q] = token_scale(p, t0 + 32 * q, 32);
+      const bool ok = tc::mbar_wait(acc_full + b, (uint32_t)(n / 2) & 1u, kWaitLimit);
+      if (!__all_sync(0xFFFFFFFFu, ok)) {
         *gave_up = 1;
         break;
       }
       tc::fence_after();
-      const uint32_t src = tmem + (uint32_t)b * kPairTok + ((uint32_t)(quarter * 32) << 16);
-      for (int j = 0; j < kPairTok; j += 16) {
-        int v[16];
-        tmem_ld16i(src + j, v);
-        if (tok * kPairTok + j < p.M) store16_any(p, c, tok * kPairTok + j, v);
+      const uint32_t src = tmem + (uint32_t)(b * kPairTok + half) + ((uint32_t)(quarter * 32) << 16);
+      int v[2][32];
+      tmem_get(src, v[0]);
+#pragma unroll
+      for (int q = 0; q < kPairTok / 64; ++q) {
+        tmem_done(v[q & 1]);
+        if (q + 1 < kPairTok / 64) {
+          tmem_get(src + 32 * (q + 1), v[(q + 1) & 1]);
+        } else {  // the columns are in registers: the next tile's MMAs may start
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_remote(mapa(tc::smem_u32(acc_empty + b), 0));
+        }
+        if (t0 + 32 * q < p.M) store_any(p, c, t0 + 32 * q, xs[q], v[q & 1]);
       }
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_remote(mapa(tc::smem_u32(acc_empty + b), 0));
     }
   }
   __syncwarp();
@@ -580,20 +661,28 @@ cudaError_t launch_split(const CUtensorMap& wmap, const CUtensorMap& xmap, LinPa
   p.ch_tiles = (p.N + kRows - 1) / kRows;
   p.tok_tiles = (p.M + kTok - 1) / kTok;
   const int64_t tiles = p.ch_tiles * p.tok_tiles;
+  if (tiles > 0x7fffffff / kMaxSplit) return cudaErrorInvalidConfiguration;
   int split = 1;
   // parts of K while the CTAs fit the SMs once and a part keeps four K blocks
-  if (Cfg::kRed > 0)
-    while (split < kMaxSplit && tiles * split * 2 <= sm_count() && p.kblocks >= 8 * split)
-      split *= 2;
-  static_assert(Cfg::kSmem <= 227 * 1024, "shared memory");
+  while (split < kMaxSplit && tiles * split * 2 <= sm_count() && p.kblocks >= 8 * split)
+    split *= 2;
+  // One CTA per SM takes all the stages that fit (or that its K needs); several
+  // share the shared memory two to an SM.
+  const int room = (tiles * split <= sm_count() ? 224 : 110) * 1024;
+  int stages = (room - Cfg::smem(0, split > 1)) / Cfg::kStage;
+  const int need = (p.kblocks + split - 1) / split;
+  stages = stages < Cfg::kMaxStages ? stages : Cfg::kMaxStages;
+  stages = stages < need ? stages : need;
+  stages = stages < 2 ? 2 : stages;
+  const int smem = Cfg::smem(stages, split > 1);
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(int8_linear_split_kernel<kTok>),
-                                   Cfg::kSmem, done);
+                                   227 * 1024, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * split));
   cfg.blockDim = dim3(kSplitThreads);
-  cfg.dynamicSmemBytes = Cfg::kSmem;
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -601,7 +690,7 @@ cudaError_t launch_split(const CUtensorMap& wmap, const CUtensorMap& xmap, LinPa
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = split > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, int8_linear_split_kernel<kTok>, wmap, xmap, p, split);
+  return cudaLaunchKernelEx(&cfg, int8_linear_split_kernel<kTok>, wmap, xmap, p, split, stages);
 }
 
 }  // namespace
