@@ -798,7 +798,7 @@ ssmq_status ssmq_int8_linear(const ssmq_linear_args* args, void* workspace, size
  * (b, d), dense; NULL h0 / dh_final: zeros.  h_final may be h0 and dh0 may be
  * dh_final (the same address).
  * lengths: device int32[b] or NULL.  Sequence i has lengths[i] steps (values
- * outside [0, L] are read as the nearest end); its other rows are not read, y
+ * outside [0, L] are read as the nearest end); its other rows are not used, y
  * and the gradients there are 0, and h_final is the state after its last step
  * (h0 for a length of 0).
  *
@@ -817,6 +817,7 @@ ssmq_status ssmq_int8_linear(const ssmq_linear_args* args, void* workspace, size
  * ssmq_gated_update: one step in place on state (fp32 (b, d), dense); seqlen
  *   is 1 and only the batch strides count.  y may be exactly z.
  *
+ * status: device word or NULL, SSMQ_DEV_TIMEOUT if a bounded device wait gave up.
  * The order of every sum depends on the sizes alone: a call repeated on the
  * same inputs gives the same bytes.  No workspace; any L >= 0, any d.
  * Errors: INVALID_ARG (NULL, negative sizes, bad strides, overlaps),
@@ -836,6 +837,7 @@ typedef struct {
   float* h_final;
   float* states;
   const int32_t* lengths;
+  uint32_t* status;
 } ssmq_gated_args;
 
 typedef struct {
@@ -847,6 +849,7 @@ typedef struct {
   const float* dh_final;
   float* dh0;
   const int32_t* lengths;
+  uint32_t* status;
 } ssmq_gated_grad_args;
 
 int32_t ssmq_gated_scan_state_steps(void);

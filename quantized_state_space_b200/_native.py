@@ -106,14 +106,14 @@ def _rows(name):
 class GatedArgs(C.Structure):
     _fields_ = [("batch", _i64), ("seqlen", _i64), ("dim", _i64), ("dtype", _i32),
                 *_rows("v"), *_rows("g"), *_rows("z"), *_rows("y"), ("h0", _vp),
-                ("h_final", _vp), ("states", _vp), ("lengths", _vp)]
+                ("h_final", _vp), ("states", _vp), ("lengths", _vp), ("status", _vp)]
 
 
 class GatedGradArgs(C.Structure):
     _fields_ = [("batch", _i64), ("seqlen", _i64), ("dim", _i64), ("dtype", _i32),
                 *_rows("v"), *_rows("g"), *_rows("z"), *_rows("dy"), *_rows("dv"), *_rows("dg"),
                 *_rows("dz"), ("states", _vp), ("dh_final", _vp), ("dh0", _vp),
-                ("lengths", _vp)]
+                ("lengths", _vp), ("status", _vp)]
 
 
 # entry point -> (restype, argtypes); every name declared in include/ssmq.h
@@ -326,8 +326,8 @@ def ssmq_state_chain(h_end, dec, n_parts, units, elems, h_out, stream=None):
 # addresses, 0 for NULL) and pack the struct in one step.
 _NORM = struct.Struct("=qqifQqQqQQqQqQqQQ").pack
 _LINEAR = struct.Struct("=qqqi4xQqQQqQQQqQ").pack
-_GATED = struct.Struct("=qqqi4x" + 4 * "Qqq" + "QQQQ").pack
-_GATED_GRAD = struct.Struct("=qqqi4x" + 7 * "Qqq" + "QQQQ").pack
+_GATED = struct.Struct("=qqqi4x" + 4 * "Qqq" + "QQQQQ").pack
+_GATED_GRAD = struct.Struct("=qqqi4x" + 7 * "Qqq" + "QQQQQ").pack
 
 
 def ssmq_rms_norm_quantize(stream, *fields):

@@ -807,7 +807,8 @@ def _saved_states(L):
     return (L + k - 1) // k
 
 
-def _gated_scan(v, g, z, h0, lengths, y, h_final, states, return_state, save_states):
+def _gated_scan(v, g, z, h0, lengths, y, h_final, states, return_state, save_states,
+                status=None):
     dv, kind = _cuda(v, "v", 3)
     shape, dt = v.shape, v.dtype
     b, L, d = shape
@@ -826,7 +827,7 @@ def _gated_scan(v, g, z, h0, lengths, y, h_final, states, return_state, save_sta
           *(_NONE if z is None else _gated_rows(z, "z", shape, dt, dv)),
           *_gated_rows(y, "y", shape, dt, dv), _dense(h0, "h0", torch.float32, b * d, dv),
           _dense(h_final, "h_final", torch.float32, b * d, dv), stp,
-          _dense(lengths, "lengths", torch.int32, b, dv))
+          _dense(lengths, "lengths", torch.int32, b, dv), _status_ptr(status, dv))
     return y, h_final, states
 
 
@@ -851,7 +852,7 @@ class _GatedScan(torch.autograd.Function):
 
 
 def gated_scan(v, g, *, z=None, h0=None, lengths=None, y=None, h_final=None, states=None,
-               return_state=True, save_states=False):
+               return_state=True, save_states=False, status=None):
     """Gated linear recurrence h_t = f_t h_{t-1} + (1 - f_t) v_t, f =
     sigmoid(g), y_t = h_t or h_t silu(z_t).
 
@@ -866,18 +867,19 @@ def gated_scan(v, g, *, z=None, h0=None, lengths=None, y=None, h_final=None, sta
     if torch.is_grad_enabled() and (v.requires_grad or g.requires_grad or
                                     (z is not None and z.requires_grad) or
                                     (h0 is not None and h0.requires_grad)):
-        if not (y is None and h_final is None and states is None and not save_states):
-            raise ValueError("y, h_final, states and save_states are for inputs without "
+        if not (y is None and h_final is None and states is None and status is None and
+                not save_states):
+            raise ValueError("y, h_final, states, status and save_states are for inputs without "
                              "requires_grad")
         out, h = _GatedScan.apply(v, g, z, h0, lengths)
         return out, (h if return_state else None)
     y, h_final, states = _gated_scan(v, g, z, h0, lengths, y, h_final, states, return_state,
-                                     save_states)
+                                     save_states, status)
     return (y, h_final, states) if states is not None else (y, h_final)
 
 
 def gated_scan_backward(dy, v, g, states, *, z=None, dh_final=None, lengths=None, dv=None,
-                        dg=None, dz=None, dh0=None):
+                        dg=None, dz=None, dh0=None, status=None):
     """Gradients (dv, dg, dz, dh0) of a gated_scan call with save_states: dy
     (b, L, d) and dh_final (b, d) float32 or None are the gradients of its
     outputs; dz is None without z.  Outputs may be given; dv, dg and dz may be
@@ -902,7 +904,7 @@ def gated_scan_backward(dy, v, g, states, *, z=None, dh_final=None, lengths=None
     _call(dev, N.ssmq_gated_scan_backward, b, L, d, kind, *rows, sp,
           _dense(dh_final, "dh_final", torch.float32, b * d, dev),
           _dense(dh0, "dh0", torch.float32, b * d, dev),
-          _dense(lengths, "lengths", torch.int32, b, dev))
+          _dense(lengths, "lengths", torch.int32, b, dev), _status_ptr(status, dev))
     return dv, dg, dz, dh0
 
 
@@ -925,5 +927,5 @@ def gated_update(state, v, g, *, z=None, y=None):
             _row_tensor(t, name, shape, dt, dv)
             rows += (t.data_ptr(), t.stride(0), d)
     _call(dv, N.ssmq_gated_update, b, 1, d, kind, *rows, 0,
-          _dense(state, "state", torch.float32, b * d, dv), 0, 0)
+          _dense(state, "state", torch.float32, b * d, dv), 0, 0, 0)
     return y

@@ -800,8 +800,10 @@ ssmq_status ssmq_gated_scan(const ssmq_gated_args* a, void* stream) {
   if (b == 0 || d == 0) return SSMQ_OK;
   REQUIRE(L == 0 || (a->v.p && a->g.p && a->y.p), SSMQ_ERR_INVALID_ARG, "%s: v, g or y is NULL",
           fn);
-  REQUIRE(aligned4(a->h0) && aligned4(a->h_final) && aligned4(a->states) && aligned4(a->lengths),
-          SSMQ_ERR_ALIGNMENT, "%s: h0, h_final, states and lengths must be 4-byte aligned", fn);
+  REQUIRE(aligned4(a->h0) && aligned4(a->h_final) && aligned4(a->states) && aligned4(a->lengths) &&
+              aligned4(a->status),
+          SSMQ_ERR_ALIGNMENT, "%s: h0, h_final, states, lengths and status must be 4-byte aligned",
+          fn);
   const int e = elem_size(a->dtype);
   const int64_t saved = (L + ssmq::kGatedStateSteps - 1) / ssmq::kGatedStateSteps;
   Named in[5] = {{"z", {}}, {"v", {}}, {"g", {}}, {"h0", dense(a->h0, 4 * b * d)},
@@ -836,8 +838,10 @@ ssmq_status ssmq_gated_scan_backward(const ssmq_gated_grad_args* a, void* stream
           SSMQ_ERR_INVALID_ARG, "%s: v, g, dy, states, dv or dg is NULL", fn);
   REQUIRE(L == 0 || (a->z.p != nullptr) == (a->dz.p != nullptr), SSMQ_ERR_INVALID_ARG,
           "%s: z and dz come together", fn);
-  REQUIRE(aligned4(a->states) && aligned4(a->dh_final) && aligned4(a->dh0) && aligned4(a->lengths),
-          SSMQ_ERR_ALIGNMENT, "%s: states, dh_final, dh0 and lengths must be 4-byte aligned", fn);
+  REQUIRE(aligned4(a->states) && aligned4(a->dh_final) && aligned4(a->dh0) &&
+              aligned4(a->lengths) && aligned4(a->status),
+          SSMQ_ERR_ALIGNMENT,
+          "%s: states, dh_final, dh0, lengths and status must be 4-byte aligned", fn);
   const int e = elem_size(a->dtype);
   const int64_t saved = (L + ssmq::kGatedStateSteps - 1) / ssmq::kGatedStateSteps;
   Named in[7] = {{"v", {}}, {"g", {}}, {"z", {}}, {"dy", {}},

@@ -23,11 +23,13 @@ struct ScanParams {
   float* h_final;
   float* states;
   const int32_t* lengths;
+  uint32_t* status;
 };
 
-template <typename T, bool kVec, int kLanes, bool kGate>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4)
-    gated_scan_kernel(const ScanParams p) {
+template <typename T, int kMode, int kLanes, bool kGate>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
+    gated_scan_kernel(const ScanParams p, const __grid_constant__ Maps maps) {
+  constexpr bool kVec = kMode != kSingle;
   __shared__ Shared<kLanes> sh;
   using TileT = Tile<kLanes>;
   const uint32_t size = cluster_size(), rank = cluster_rank();
@@ -53,29 +55,51 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4)
   float2 h = make_float2(0.0f, 0.0f);
   if (p.h0) h = make_float2(p.h0[seq * p.d + c0], p.h0[seq * p.d + c0 + next]);
 
-  extern __shared__ __align__(16) uint8_t slots[];
-  using St = Stage<T, kGate ? 3 : 2>;
+  extern __shared__ __align__(128) uint8_t slots[];
+  constexpr int kTensors = kGate ? 3 : 2;
+  using St = Stage<T, kTensors, kMode, kLanes>;
   const St stage(slots);
+  __shared__ uint64_t full[St::kBufs];
   const int64_t rounds = (p.tiles + size - 1) / size;
+  uint32_t flags = 0;
   auto fetch = [&](int64_t k) {
-    const int64_t t0 = (k * size + rank) * TileT::kLen + first;
-    const int left = rows_left(end, t0), buf = (int)(k & 1);
-    stage.template fetch<kVec>(buf, 0, gp + t0 * p.g.rs, p.g.rs, next, left);
-    stage.template fetch<kVec>(buf, 1, vp + t0 * p.v.rs, p.v.rs, next, left);
-    if constexpr (kGate) stage.template fetch<kVec>(buf, 2, zp + t0 * p.z.rs, p.z.rs, next, left);
-    St::commit();
-  };
-  if (St::kBufs == 2 && rounds > 0) fetch(0);
-  for (int64_t k = 0; k < rounds; ++k) {
-    const int buf = (int)(k & 1);
-    if (St::kBufs == 1) {
-      fetch(k);
-      St::template wait<0>();
-    } else if (k + 1 < rounds) {
-      fetch(k + 1);
-      St::template wait<1>();
+    if (k >= rounds) {
+      if constexpr (kMode != kTma) St::commit();
+      return;
+    }
+    const int buf = (int)(k % St::kBufs);
+    if constexpr (kMode == kTma) {
+      if (threadIdx.x == 0) {
+        const int c = (int)(blk * TileT::kChannels), t = (int)((k * size + rank) * TileT::kLen);
+        stream::expect_tx(full + buf, kTensors * St::kTensorBytes);
+#pragma unroll
+        for (int i = 0; i < kTensors; ++i)
+          St::fetch_tile(slots, buf, i, maps.m + i, c, t, (int)seq, full + buf);
+      }
     } else {
-      St::template wait<0>();
+      const int64_t t0 = (k * size + rank) * TileT::kLen + first;
+      const int left = rows_left(end, t0);
+      stage.fetch(buf, 0, gp + t0 * p.g.rs, p.g.rs, next, left);
+      stage.fetch(buf, 1, vp + t0 * p.v.rs, p.v.rs, next, left);
+      if constexpr (kGate) stage.fetch(buf, 2, zp + t0 * p.z.rs, p.z.rs, next, left);
+      St::commit();
+    }
+  };
+  if constexpr (kMode == kTma) {
+    if (threadIdx.x == 0)
+      for (int i = 0; i < St::kBufs; ++i) tc::mbar_init(full + i, 1);
+    __syncthreads();
+  }
+  carry_init(sh, size);
+  for (int k = 0; k < St::kAhead; ++k) fetch(k);
+  for (int64_t k = 0; k < rounds; ++k) {
+    const int buf = (int)(k % St::kBufs);
+    if constexpr (kMode == kTma) {
+      if (!tc::mbar_wait(full + buf, (uint32_t)(k / St::kBufs) & 1u, kWaitLimit))
+        flags |= SSMQ_DEV_TIMEOUT;
+    } else {
+      fetch(k + St::kAhead);
+      St::wait();
     }
     const int64_t t0 = (k * size + rank) * TileT::kLen + first;
     float2 f[kSteps], u[kSteps];
@@ -99,8 +123,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4)
       a = fmul2(a, f[i]);
       b = ffma2(f[i], b, u[i]);
     }
-    float2 s = carry_in<kLanes, false>(sh, buf, make_float4(a.x, a.y, b.x, b.y), h, rank,
-                                       size);
+    float2 s = carry_in<kLanes, false>(sh, k, make_float4(a.x, a.y, b.x, b.y), h, rank,
+                                       size, flags, [&] {
+                                         // (the tile before this one is read: its buffer is free)
+                                         if constexpr (kMode == kTma) fetch(k + St::kAhead);
+                                       });
     if (p.states && t0 < p.L && t0 % kGatedStateSteps == 0) {
       float* o = p.states + (seq * p.saved + t0 / kGatedStateSteps) * p.d + c0;
       if (in0) o[0] = s.x;
@@ -133,6 +160,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4)
     if (in0) o[0] = h.x;
     if (in1) o[next] = h.y;
   }
+  flag_status(p.status, flags);
+  carry_done(size);
 }
 
 template <typename T>
@@ -153,19 +182,30 @@ cudaError_t scan_type(const ssmq_gated_args& a, cudaStream_t st) {
   p.h_final = a.h_final;
   p.states = a.states;
   p.lengths = a.lengths;
+  p.status = a.status;
   const bool vec = a.dim % 2 == 0 && pairs_ok<T>(a.v) && pairs_ok<T>(a.g) && pairs_ok<T>(a.z) &&
                    pairs_ok<T>(a.y);
   const bool z = a.z.p != nullptr;
-#define SSMQ_GATED(V, N, Z) \
-  return launch<gated_scan_kernel<T, V, N, Z>>(p, s, Stage<T, Z ? 3 : 2>::kBytes, st)
-  if (vec) {
-    if (s.narrow) { if (z) SSMQ_GATED(true, 8, true); SSMQ_GATED(true, 8, false); }
-    if (z) SSMQ_GATED(true, 32, true);
-    SSMQ_GATED(true, 32, false);
+  Maps maps = {};
+  const int ch = s.narrow ? Tile<8>::kChannels : Tile<32>::kChannels;
+  auto map = [&](int i, const ssmq_rows& r) {
+    return map_rows<T>(maps.m + i, r, a.batch, a.seqlen, a.dim, ch, len);
+  };
+  const int mode = !vec ? kSingle
+                        : (map(0, a.g) && map(1, a.v) && (!z || map(2, a.z)) ? kTma : kPairs);
+#define SSMQ_GATED(M, N, Z)                       \
+  return launch<gated_scan_kernel<T, M, N, Z>>(p, maps, s, Stage<T, Z ? 3 : 2, M, N>::kBytes, st)
+#define SSMQ_GATED_N(N)                                          \
+  switch (mode) {                                                \
+    case kTma: if (z) SSMQ_GATED(kTma, N, true); SSMQ_GATED(kTma, N, false);       \
+    case kPairs: if (z) SSMQ_GATED(kPairs, N, true); SSMQ_GATED(kPairs, N, false); \
+    default: if (z) SSMQ_GATED(kSingle, N, true); SSMQ_GATED(kSingle, N, false);   \
   }
-  if (s.narrow) { if (z) SSMQ_GATED(false, 8, true); SSMQ_GATED(false, 8, false); }
-  if (z) SSMQ_GATED(false, 32, true);
-  SSMQ_GATED(false, 32, false);
+  if (s.narrow) {
+    SSMQ_GATED_N(8)
+  }
+  SSMQ_GATED_N(32)
+#undef SSMQ_GATED_N
 #undef SSMQ_GATED
 }
 

@@ -8,12 +8,14 @@
 // and the CTA kWarps * 32 / kLanes.  A segment acts on the state entering it
 // as h -> A h + B; (A, B) of segments, warps and CTAs compose in step order.
 // The CTAs of a cluster hold consecutive tiles and push their (A, B) into
-// each other's shared memory; one cluster barrier per round replaces a pass
-// over the data or a spin on global memory.
+// each other's shared memory; one exchange per round replaces a pass over the
+// data or a spin on global memory.
 #pragma once
 
 #include "internal.h"
+#include "stream.cuh"
 #include "tc.cuh"
+#include "tma_map.h"
 #include "vec8.cuh"
 
 namespace ssmq {
@@ -22,7 +24,15 @@ namespace gated {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSteps = 8;        // consecutive steps per thread
-constexpr int kMaxCluster = 8;   // CTAs along time (portable cluster size)
+constexpr int kMaxCluster = 16;  // CTAs along time (above 8: non-portable)
+constexpr uint32_t kWaitLimit = 1u << 20;
+
+// How a tile's inputs reach shared memory.
+enum {
+  kTma = 0,    // whole tiles by TMA: rows on 16-byte boundaries
+  kPairs = 1,  // each thread its own pairs of channels
+  kSingle = 2  // each thread its own channels one by one
+};
 
 template <int kLanes>
 struct Tile {
@@ -54,20 +64,7 @@ __device__ __forceinline__ float2 pair_f32(Pair<T> p) { return unpack2<T>(p.w); 
 template <>
 __device__ __forceinline__ float2 pair_f32<float>(Pair<float> p) { return p.w; }
 
-// Elements p[0] and p[next] (kVec: one load of a pair).
-template <typename T, bool kVec>
-__device__ __forceinline__ Pair<T> load_pair(const T* p, int next) {
-  Pair<T> r;
-  if constexpr (kVec) {
-    r = *reinterpret_cast<const Pair<T>*>(p);
-  } else if constexpr (sizeof(T) == 4) {
-    r.w = make_float2(p[0], p[next]);
-  } else {
-    const uint16_t* u = reinterpret_cast<const uint16_t*>(p);
-    r.w = (uint32_t)u[0] | ((uint32_t)u[next] << 16);
-  }
-  return r;
-}
+// Elements p[0] and p[next] (kVec: one store of a pair).
 template <typename T, bool kVec>
 __device__ __forceinline__ void store_pair(T* p, int next, float2 v, bool in0, bool in1) {
   if constexpr (kVec) {
@@ -83,57 +80,101 @@ __device__ __forceinline__ void store_pair(T* p, int next, float2 v, bool in0, b
   }
 }
 
-// Staged inputs.  Every thread copies the pairs of its own steps into slots of
-// its own ([buffer][tensor][step][thread], conflict-free) one round ahead and
-// reads them back itself: no barrier, and no registers held by loads in flight.
-template <typename T, int kTensors>
+struct Maps {
+  CUtensorMap m[4];
+};
+
+// Staged inputs: kBufs tiles of kTensors tensors in shared memory, filled ahead
+// of the round that reads them, so that no register holds a load in flight.
+// kTma: one thread fetches whole tiles ([row][channel]); rows and channels
+// beyond the tensor read as zero.  Otherwise every thread copies the pairs of
+// its own steps into slots of its own ([step][thread]).  Either way a thread
+// reads only its own steps and channels.
+template <typename T, int kTensors, int kMode, int kLanes>
 struct Stage {
-  // two buffers of 16-bit elements; binary32 has room for one
-  static constexpr int kBufs = sizeof(T) == 4 ? 1 : 2;
-  static constexpr int kPerBuf = kTensors * kSteps * kThreads;
-  static constexpr int kBytes = kBufs * kPerBuf * (int)sizeof(Pair<T>);
-  Pair<T>* mine;
-  __device__ __forceinline__ Stage(void* smem)
-      : mine(static_cast<Pair<T>*>(smem) + threadIdx.x) {}
-  __device__ __forceinline__ Pair<T>* at(int buf, int tensor) const {
-    return mine + (kBufs == 1 ? 0 : buf) * kPerBuf + tensor * kSteps * kThreads;
+  using TileT = Tile<kLanes>;
+  // (two or three CTAs' buffers fit an SM)
+  static constexpr int kBufs =
+      kMode == kTma ? (sizeof(T) == 2 && kTensors == 2 ? 3 : 2) : (sizeof(T) == 4 ? 1 : 2);
+  static_assert(kMode != kTma || kBufs > 1, "a tile is fetched while another is read");
+  static constexpr int kAhead = kBufs > 1 ? kBufs - 1 : 0;  // rounds fetched ahead
+  static constexpr int kTensorBytes = TileT::kLen * TileT::kChannels * (int)sizeof(T);
+  static constexpr int kStepBytes =
+      (kMode == kTma ? TileT::kChannels : 2 * kThreads) * (int)sizeof(T);
+  static constexpr int kBytes = kBufs * kTensors * kTensorBytes;
+  uint8_t* base;  // of this thread's pairs
+  __device__ __forceinline__ explicit Stage(uint8_t* smem) {
+    if constexpr (kMode == kTma) {
+      const int lane = threadIdx.x & 31;
+      const int row = ((int)(threadIdx.x >> 5) * TileT::kSubs + lane / kLanes) * kSteps;
+      base = smem + row * kStepBytes + (lane % kLanes) * 2 * (int)sizeof(T);
+    } else {
+      base = smem + threadIdx.x * 2 * (int)sizeof(T);
+    }
+  }
+  __device__ __forceinline__ uint8_t* at(int buf, int tensor) const {
+    return base + (buf * kTensors + tensor) * kTensorBytes;
   }
   __device__ __forceinline__ float2 get(int buf, int tensor, int i) const {
-    return pair_f32<T>(at(buf, tensor)[i * kThreads]);
+    return pair_f32<T>(*reinterpret_cast<const Pair<T>*>(at(buf, tensor) + i * kStepBytes));
   }
-  // rows 0 .. left - 1 of the thread's steps, zeros behind them.  Lanes without
-  // a channel have their pointers clamped to channel 0.
-  template <bool kVec>
+  // kTma: the tile at (channel c, step t, sequence s) of one tensor
+  static __device__ __forceinline__ void fetch_tile(uint8_t* smem, int buf, int tensor,
+                                                    const CUtensorMap* map, int c, int t, int s,
+                                                    uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4}], [%5];" ::"r"(
+            tc::smem_u32(smem + (buf * kTensors + tensor) * kTensorBytes)),
+        "l"(map), "r"(c), "r"(t), "r"(s), "r"(tc::smem_u32(bar))
+        : "memory");
+  }
+  // the other modes: rows 0 .. left - 1 of the thread's steps, zeros behind
+  // them.  Lanes without a channel have their pointers clamped to channel 0.
   __device__ __forceinline__ void fetch(int buf, int tensor, const T* p, int64_t rs, int next,
                                         int left) const {
-    Pair<T>* o = at(buf, tensor);
-    if constexpr (kVec) {
+    uint8_t* o = at(buf, tensor);
+    if constexpr (kMode == kPairs || sizeof(T) == 4) {
+      constexpr int kN = kMode == kPairs ? 1 : 2;  // copies per pair
+      constexpr int kCopy = 2 * (int)sizeof(T) / kN;
       const uint32_t dst = tc::smem_u32(o);
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        const int bytes = i < left ? (int)sizeof(Pair<T>) : 0;
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(
-                         dst + i * kThreads * (int)sizeof(Pair<T>)),
-                     "l"(p + i * rs), "n"(sizeof(Pair<T>)), "r"(bytes)
-                     : "memory");
+        const int bytes = i < left ? kCopy : 0;
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(
+                           dst + i * kStepBytes + j * kCopy),
+                       "l"(p + i * rs + j * next), "n"(kCopy), "r"(bytes)
+                       : "memory");
       }
     } else {
-      Pair<T> r[kSteps];
+      uint32_t r[kSteps];
+      const uint16_t* u = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        r[i] = Pair<T>{};
-        if (i < left) r[i] = load_pair<T, kVec>(p + i * rs, next);
+        r[i] = 0;
+        if (i < left) r[i] = (uint32_t)u[i * rs] | ((uint32_t)u[i * rs + next] << 16);
       }
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) o[i * kThreads] = r[i];
+      for (int i = 0; i < kSteps; ++i) *reinterpret_cast<uint32_t*>(o + i * kStepBytes) = r[i];
     }
+  }
+  // zeros in the thread's steps from `left` on: tiles by TMA bring the rows
+  // behind a sequence's end, and no tile brings those in front of its start
+  __device__ __forceinline__ void clear(int buf, int left) const {
+    for (int j = 0; j < kTensors; ++j)
+      for (int i = left; i < kSteps; ++i)
+        *reinterpret_cast<Pair<T>*>(at(buf, j) + i * kStepBytes) = Pair<T>{};
+    // (a later tile's copy into this buffer comes after these stores)
+    tc::fence_async_smem();
   }
   static __device__ __forceinline__ void commit() {
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  template <int kPending>
+  // all but the newest kAhead groups have landed
   static __device__ __forceinline__ void wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
   }
 };
 // rows of the segment at t0 that lie before the end, at most kSteps
@@ -178,13 +219,24 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// 16 bytes into the same shared-memory location of CTA `rank` of the cluster
-__device__ __forceinline__ void push_f4(float4* local, uint32_t rank, float4 v) {
-  uint32_t a;
+// Barriers at both ends of the kernel.  (Inside, states travel by st.async with
+// an mbarrier at the receiver: a cluster barrier with release semantics would
+// wait for the round's stores to global memory as well.)
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+// 16 bytes into the same shared-memory location of CTA `rank` of the cluster,
+// counted on the same barrier there
+__device__ __forceinline__ void push_f4(float4* local, uint64_t* bar, uint32_t rank, float4 v) {
+  uint32_t a, b;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::smem_u32(local)), "r"(rank));
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y),
-               "f"(v.z), "f"(v.w)
-               : "memory");
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(tc::smem_u32(bar)), "r"(rank));
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, "
+      "[%5];" ::"r"(a),
+      "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(b)
+      : "memory");
 }
 
 // (A, B) of two channels: {A0, A1, B0, B1}; h -> A h + B
@@ -205,16 +257,38 @@ __device__ __forceinline__ float4 shfl_f4(float4 v, int src) {
 template <int kLanes>
 struct Shared {
   float4 warp[2][kWarps][kLanes];
-  float4 cta[2][kMaxCluster][kLanes];
+  float4 cta[2][kLanes == 32 ? 8 : kMaxCluster][kLanes];  // (wide blocks: portable clusters)
+  uint64_t bar[2];  // the maps of all CTAs of a round have arrived
 };
+
+// Before the first round (every thread of the cluster).
+template <int kLanes>
+__device__ __forceinline__ void carry_init(Shared<kLanes>& sh, uint32_t size) {
+  if (size == 1) return;
+  if (threadIdx.x == 0) {
+    tc::mbar_init(sh.bar, 1);
+    tc::mbar_init(sh.bar + 1, 1);
+  }
+  cluster_sync();
+}
+// Behind the last one: nobody pushes to a CTA that has left.
+__device__ __forceinline__ void carry_done(uint32_t size) {
+  __syncwarp();
+  if (size > 1) cluster_meet();
+}
 
 // State entering this thread's segment, from the segments' maps in step order
 // (kReverse: in reverse step order, the last segment of the warp, warp and
 // CTA first), and the state behind the whole round in h.  Every thread of the
-// cluster calls it; buf alternates between rounds.
-template <int kLanes, bool kReverse>
-__device__ __forceinline__ float2 carry_in(Shared<kLanes>& sh, int buf, float4 m, float2& h,
-                                           uint32_t rank, uint32_t size) {
+// cluster calls it, round by round.  Buffers alternate between rounds: a CTA pushes
+// round k + 2 only after it has every map of round k + 1, and a CTA pushes
+// round k + 1 only when its threads are done with round k.  met() runs behind the CTA's
+// barrier: every thread is done with the rounds before this one.
+template <int kLanes, bool kReverse, typename Met>
+__device__ __forceinline__ float2 carry_in(Shared<kLanes>& sh, int64_t k, float4 m, float2& h,
+                                           uint32_t rank, uint32_t size, uint32_t& flags,
+                                           Met met) {
+  const int buf = (int)(k & 1);
   constexpr int kSubs = 32 / kLanes;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub0 = lane / kLanes, l = lane % kLanes;
@@ -235,6 +309,7 @@ __device__ __forceinline__ float2 carry_in(Shared<kLanes>& sh, int buf, float4 m
     if (sub > 0) mine = before;
   }
   __syncthreads();
+  met();
   float4 pre = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
 #pragma unroll 1
   for (int i = 0; i < w; ++i) pre = compose(pre, sh.warp[buf][i][l]);
@@ -243,9 +318,15 @@ __device__ __forceinline__ float2 carry_in(Shared<kLanes>& sh, int buf, float4 m
   for (int i = w; i < kWarps; ++i) all = compose(all, sh.warp[buf][i][l]);
   float2 base = h;
   if (size > 1) {
-    // warp i tells CTA i of the cluster what this CTA's tile does to a state
-    if ((uint32_t)warp < size && sub0 == 0) push_f4(&sh.cta[buf][rank][l], (uint32_t)warp, all);
-    cluster_sync();
+    // warp i tells CTA i (and i + 8) of the cluster what this CTA's tile does to a state
+    if (threadIdx.x == 0)
+      stream::expect_tx(sh.bar + buf, size * kLanes * (uint32_t)sizeof(float4));
+    if (sub0 == 0)
+      for (uint32_t r = (uint32_t)warp; r < size; r += kWarps)
+        push_f4(&sh.cta[buf][rank][l], sh.bar + buf, r, all);
+    if (!tc::mbar_wait(sh.bar + buf, (uint32_t)(k >> 1) & 1u, kWaitLimit))
+      flags |= SSMQ_DEV_TIMEOUT;
+    __syncwarp();
     float2 s = h;
     for (uint32_t r = 0; r < size; ++r) {
       if (r == rank) base = s;
@@ -268,22 +349,23 @@ struct Shape {
 inline Shape shape_for(int64_t b, int64_t L, int64_t d) {
   Shape s;
   // Enough CTAs for eight per SM, first by splitting time over a cluster, then
-  // by narrower channel blocks (32-byte rows of 16-bit elements).
+  // by narrower channel blocks (32-byte rows of 16-bit elements), then by
+  // clusters of 16.
   const int64_t want = 8 * (int64_t)sm_count();
-  auto pick = [&](int channels, int len) {
+  auto pick = [&](int channels, int len, int most) {
     s.blocks = (d + channels - 1) / channels;
     const int64_t tiles = (L + len - 1) / len;
     s.cluster = 1;
-    while (s.cluster < kMaxCluster && s.cluster < tiles && b * s.blocks * s.cluster < want)
+    while (s.cluster < most && s.cluster < tiles && b * s.blocks * s.cluster < want)
       s.cluster *= 2;
     return b * s.blocks * s.cluster;
   };
   s.narrow = false;
-  int64_t n = pick(Tile<32>::kChannels, Tile<32>::kLen);
+  int64_t n = pick(Tile<32>::kChannels, Tile<32>::kLen, 8);
   if (n < want / 4) {
     const Shape wide = s;
     s.narrow = true;
-    const int64_t m = pick(Tile<8>::kChannels, Tile<8>::kLen);
+    const int64_t m = pick(Tile<8>::kChannels, Tile<8>::kLen, kMaxCluster);
     if (m <= n || L <= Tile<8>::kLen / 2) s = wide;
     else n = m;
   }
@@ -292,9 +374,10 @@ inline Shape shape_for(int64_t b, int64_t L, int64_t d) {
 }
 
 template <auto kern, typename Params>
-cudaError_t launch(const Params& p, const Shape& s, int smem, cudaStream_t st) {
-  static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, done);
+cudaError_t launch(const Params& p, const Maps& maps, const Shape& s, int smem, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0}, wide{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, done);
+  if (e == cudaSuccess && s.cluster > 8) e = allow_wide_cluster(reinterpret_cast<const void*>(kern), wide);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(s.grid);
@@ -307,13 +390,35 @@ cudaError_t launch(const Params& p, const Shape& s, int smem, cudaStream_t st) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = s.cluster > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, p);
+  return cudaLaunchKernelEx(&cfg, kern, p, maps);
 }
 
 template <typename T>
 bool pairs_ok(const ssmq_rows& r) {
   return !r.p || ((reinterpret_cast<uintptr_t>(r.p) % (2 * sizeof(T))) == 0 &&
                   r.batch_stride % 2 == 0 && r.row_stride % 2 == 0);
+}
+
+// Tensor map of a (b, L, d) tensor with boxes of one tile; false when TMA does
+// not take it (rows off 16-byte boundaries, a broadcast batch, huge sizes).
+template <typename T>
+bool map_rows(CUtensorMap* map, const ssmq_rows& r, int64_t b, int64_t L, int64_t d, int channels,
+              int len) {
+  const EncodeFn fn = tensor_map_encoder();
+  const int64_t rs = (L > 1 ? r.row_stride : (d + 7) / 8 * 8) * (int64_t)sizeof(T);
+  const int64_t bs = b > 1 ? r.batch_stride * (int64_t)sizeof(T) : rs * L;
+  const int64_t most = (int64_t)1 << 40;
+  if (!fn || (reinterpret_cast<uintptr_t>(r.p) & 15u) || rs % 16 || bs % 16 || rs <= 0 ||
+      bs <= 0 || rs >= most || bs >= most || L >= ((int64_t)1 << 31) - 65536)
+    return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)L, (cuuint64_t)b};
+  const cuuint64_t strides[2] = {(cuuint64_t)rs, (cuuint64_t)bs};
+  const cuuint32_t box[3] = {(cuuint32_t)channels, (cuuint32_t)len, 1};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return fn(map, sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3,
+            r.p, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace gated

@@ -27,10 +27,13 @@ struct GradParams {
   const float* dh_final;
   float* dh0;
   const int32_t* lengths;
+  uint32_t* status;
 };
 
-template <typename T, bool kVec, int kLanes, bool kGate>
-__global__ void __launch_bounds__(kThreads, 2) gated_scan_grad_kernel(const GradParams p) {
+template <typename T, int kMode, int kLanes, bool kGate>
+__global__ void __launch_bounds__(kThreads, 2)
+    gated_scan_grad_kernel(const GradParams p, const __grid_constant__ Maps maps) {
+  constexpr bool kVec = kMode != kSingle;
   __shared__ Shared<kLanes> sh;
   __shared__ float4 s_fwd[2][kWarps][kLanes];
   using TileT = Tile<kLanes>;
@@ -61,38 +64,61 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_grad_kernel(const Grad
   if (p.dh_final)
     c = make_float2(p.dh_final[seq * p.d + c0], p.dh_final[seq * p.d + c0 + next]);
 
-  extern __shared__ __align__(16) uint8_t slots[];
-  using St = Stage<T, kGate ? 4 : 3>;
+  extern __shared__ __align__(128) uint8_t slots[];
+  constexpr int kTensors = kGate ? 4 : 3;
+  using St = Stage<T, kTensors, kMode, kLanes>;
   const St stage(slots);
+  __shared__ uint64_t full[St::kBufs];
   const int64_t rounds = (p.tiles + size - 1) / size;
+  uint32_t flags = 0;
   // tiles from the last one backwards; rank 0 holds the latest of a round
   auto tile_of = [&](int64_t k) { return p.tiles - 1 - (k * size + rank); };
   auto fetch = [&](int64_t k) {
     const int64_t tile = tile_of(k);
-    const int64_t t0 = tile >= 0 ? tile * TileT::kLen + first : 0;
-    const int left = tile >= 0 ? rows_left(end, t0) : 0, buf = (int)(k & 1);
-    stage.template fetch<kVec>(buf, 0, gp + t0 * p.g.rs, p.g.rs, next, left);
-    stage.template fetch<kVec>(buf, 1, vp + t0 * p.v.rs, p.v.rs, next, left);
-    stage.template fetch<kVec>(buf, 2, dyp + t0 * p.dy.rs, p.dy.rs, next, left);
-    if constexpr (kGate) stage.template fetch<kVec>(buf, 3, zp + t0 * p.z.rs, p.z.rs, next, left);
-    St::commit();
-  };
-  if (St::kBufs == 2 && rounds > 0) fetch(0);
-  for (int64_t k = 0; k < rounds; ++k) {
-    const int buf = (int)(k & 1);
-    if (St::kBufs == 1) {
-      fetch(k);
-      St::template wait<0>();
-    } else if (k + 1 < rounds) {
-      fetch(k + 1);
-      St::template wait<1>();
+    const int buf = (int)(k % St::kBufs);
+    if constexpr (kMode == kTma) {
+      if (threadIdx.x == 0 && k < rounds && tile >= 0) {
+        const int c = (int)(blk * TileT::kChannels), t = (int)(tile * TileT::kLen);
+        stream::expect_tx(full + buf, kTensors * St::kTensorBytes);
+#pragma unroll
+        for (int i = 0; i < kTensors; ++i)
+          St::fetch_tile(slots, buf, i, maps.m + i, c, t, (int)seq, full + buf);
+      }
     } else {
-      St::template wait<0>();
+      if (k < rounds) {
+        const int64_t t0 = tile >= 0 ? tile * TileT::kLen + first : 0;
+        const int left = tile >= 0 ? rows_left(end, t0) : 0;
+        stage.fetch(buf, 0, gp + t0 * p.g.rs, p.g.rs, next, left);
+        stage.fetch(buf, 1, vp + t0 * p.v.rs, p.v.rs, next, left);
+        stage.fetch(buf, 2, dyp + t0 * p.dy.rs, p.dy.rs, next, left);
+        if constexpr (kGate) stage.fetch(buf, 3, zp + t0 * p.z.rs, p.z.rs, next, left);
+      }
+      St::commit();
+    }
+  };
+  if constexpr (kMode == kTma) {
+    if (threadIdx.x == 0)
+      for (int i = 0; i < St::kBufs; ++i) tc::mbar_init(full + i, 1);
+    __syncthreads();
+  }
+  carry_init(sh, size);
+  for (int k = 0; k < St::kAhead; ++k) fetch(k);
+  for (int64_t k = 0; k < rounds; ++k) {
+    const int buf = (int)(k % St::kBufs);
+    if constexpr (kMode == kTma) {
+      if (tile_of(k) >= 0 &&
+          !tc::mbar_wait(full + buf, (uint32_t)(k / St::kBufs) & 1u, kWaitLimit))
+        flags |= SSMQ_DEV_TIMEOUT;
+    } else {
+      fetch(k + St::kAhead);
+      St::wait();
     }
     const int64_t tile = tile_of(k);
     const bool real = tile >= 0;
     const int64_t t0 = real ? tile * TileT::kLen + first : 0;
     const int left = real ? rows_left(end, t0) : 0;
+    if constexpr (kMode == kTma)
+      if (left < kSteps) stage.clear(buf, left);
     float2 hs = make_float2(0.0f, 0.0f);  // state before the tile
     if (real) {
       const float* sp = p.states +
@@ -138,16 +164,19 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_grad_kernel(const Grad
         const float4 before = shfl_f4(m, (lane - o * kLanes) & 31);
         if (sub >= o) m = compose(before, m);
       }
-      if (sub == kSubs - 1) s_fwd[buf][warp][l] = m;
+      if (sub == kSubs - 1) s_fwd[k & 1][warp][l] = m;
       float4 mine = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
       if constexpr (kSubs > 1) {
         const float4 before = shfl_f4(m, (lane - kLanes) & 31);
         if (sub > 0) mine = before;
       }
       // (the barrier inside carry_in orders s_fwd as well)
-      r = carry_in<kLanes, true>(sh, buf, make_float4(a.x, a.y, r.x, r.y), c, rank, size);
+      r = carry_in<kLanes, true>(sh, k, make_float4(a.x, a.y, r.x, r.y), c, rank, size, flags,
+                                 [&] {
+                                   if constexpr (kMode == kTma) fetch(k + St::kAhead);
+                                 });
 #pragma unroll 1
-      for (int w = 0; w < warp; ++w) hs = apply(s_fwd[buf][w][l], hs);
+      for (int w = 0; w < warp; ++w) hs = apply(s_fwd[k & 1][w][l], hs);
       hs = apply(mine, hs);
     }
 
@@ -194,6 +223,8 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_grad_kernel(const Grad
     if (in0) o[0] = c.x;
     if (in1) o[next] = c.y;
   }
+  flag_status(p.status, flags);
+  carry_done(size);
 }
 
 template <typename T>
@@ -217,20 +248,34 @@ cudaError_t grad_type(const ssmq_gated_grad_args& a, cudaStream_t st) {
   p.dh_final = a.dh_final;
   p.dh0 = a.dh0;
   p.lengths = a.lengths;
+  p.status = a.status;
   const bool z = a.z.p != nullptr;
   const bool vec = a.dim % 2 == 0 && pairs_ok<T>(a.v) && pairs_ok<T>(a.g) && pairs_ok<T>(a.dy) &&
                    pairs_ok<T>(a.dv) && pairs_ok<T>(a.dg) &&
                    (!z || (pairs_ok<T>(a.z) && pairs_ok<T>(a.dz)));
-#define SSMQ_GATED(V, N, Z) \
-  return launch<gated_scan_grad_kernel<T, V, N, Z>>(p, s, Stage<T, Z ? 4 : 3>::kBytes, st)
-  if (vec) {
-    if (s.narrow) { if (z) SSMQ_GATED(true, 8, true); SSMQ_GATED(true, 8, false); }
-    if (z) SSMQ_GATED(true, 32, true);
-    SSMQ_GATED(true, 32, false);
+  Maps maps = {};
+  const int ch = s.narrow ? Tile<8>::kChannels : Tile<32>::kChannels;
+  auto map = [&](int i, const ssmq_rows& r) {
+    return map_rows<T>(maps.m + i, r, a.batch, a.seqlen, a.dim, ch, len);
+  };
+  const int mode = !vec ? kSingle
+                        : (map(0, a.g) && map(1, a.v) && map(2, a.dy) && (!z || map(3, a.z))
+                               ? kTma
+                               : kPairs);
+#define SSMQ_GATED(M, N, Z)                                                                  \
+  return launch<gated_scan_grad_kernel<T, M, N, Z>>(p, maps, s, Stage<T, Z ? 4 : 3, M, N>::kBytes, \
+                                                    st)
+#define SSMQ_GATED_N(N)                                          \
+  switch (mode) {                                                \
+    case kTma: if (z) SSMQ_GATED(kTma, N, true); SSMQ_GATED(kTma, N, false);       \
+    case kPairs: if (z) SSMQ_GATED(kPairs, N, true); SSMQ_GATED(kPairs, N, false); \
+    default: if (z) SSMQ_GATED(kSingle, N, true); SSMQ_GATED(kSingle, N, false);   \
   }
-  if (s.narrow) { if (z) SSMQ_GATED(false, 8, true); SSMQ_GATED(false, 8, false); }
-  if (z) SSMQ_GATED(false, 32, true);
-  SSMQ_GATED(false, 32, false);
+  if (s.narrow) {
+    SSMQ_GATED_N(8)
+  }
+  SSMQ_GATED_N(32)
+#undef SSMQ_GATED_N
 #undef SSMQ_GATED
 }
 

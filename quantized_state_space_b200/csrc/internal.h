@@ -90,6 +90,19 @@ inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_
   return e;
 }
 
+// The same for clusters of more than eight CTAs.
+inline cudaError_t allow_wide_cluster(const void* kernel, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  const cudaError_t g = cudaGetDevice(&dev);
+  if (g != cudaSuccess) return g;
+  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 size_t ssd_workspace_bytes(const ssmq_ssd_args& a);
 cudaError_t launch_ssd(const ssmq_ssd_args& a, void* ws, cudaStream_t st);
 cudaError_t launch_ssd_carry_in(const ssmq_ssd_args& a, const float* h_carry, void* ws,

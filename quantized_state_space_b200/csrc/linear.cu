@@ -16,11 +16,10 @@
 // Both operands are K-major, brought in by TMA as 128-byte rows in the
 // 128-byte swizzle (32 bytes, one MMA K-step, per quarter row); rows and
 // columns beyond the tensor read as zero.
-#include <cuda.h>
-
 #include "internal.h"
 #include "stream.cuh"
 #include "tc.cuh"
+#include "tma_map.h"
 #include "vec8.cuh"
 
 namespace ssmq {
@@ -618,29 +617,9 @@ bool tma_rows(const void* p, int64_t rows, int64_t stride) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (rows <= 1 || stride % 16 == 0);
 }
 
-typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                             const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                             const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// cuTensorMapEncodeTiled, looked up once per process (a driver entry point: the
-// library does not link libcuda)
-EncodeFn encode_fn() {
-  static const EncodeFn fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<EncodeFn>(f);
-  }();
-  return fn;
-}
-
 cudaError_t encode(CUtensorMap* map, const void* p, int64_t rows, int64_t k, int64_t stride,
                    int box_rows) {
-  const EncodeFn fn = encode_fn();
+  const EncodeFn fn = tensor_map_encoder();
   if (!fn) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows};
   // (one row: its stride is never used, but has to be a multiple of 16)
