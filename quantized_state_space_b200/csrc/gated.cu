@@ -14,6 +14,13 @@ namespace {
 
 using namespace gated;
 
+// Four warps of sixteen steps: with eight warps of eight the exchange between
+// segments weighed more than the steps (8 x 2048 x 1536 binary16, gated: 53 us
+// against 45), and with them three CTAs share an SM.
+template <int kLanes>
+using ScanTile = Tile<4, 16, kLanes>;
+constexpr int kScanCtas = 3;  // per SM
+
 struct ScanParams {
   int64_t L, d, blocks;
   int64_t tiles;        // time tiles of a sequence
@@ -27,11 +34,12 @@ struct ScanParams {
 };
 
 template <typename T, int kMode, int kLanes, bool kGate>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
+__global__ void __launch_bounds__(ScanTile<kLanes>::kThreads, kScanCtas)
     gated_scan_kernel(const ScanParams p, const __grid_constant__ Maps maps) {
   constexpr bool kVec = kMode != kSingle;
-  __shared__ Shared<kLanes> sh;
-  using TileT = Tile<kLanes>;
+  using TileT = ScanTile<kLanes>;
+  constexpr int kSteps = TileT::kSteps;
+  __shared__ Shared<TileT> sh;
   const uint32_t size = cluster_size(), rank = cluster_rank();
   const int64_t unit = blockIdx.x / size;  // (sequence, channel block)
   const int64_t seq = unit / p.blocks, blk = unit % p.blocks;
@@ -57,7 +65,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
 
   extern __shared__ __align__(128) uint8_t slots[];
   constexpr int kTensors = kGate ? 3 : 2;
-  using St = Stage<T, kTensors, kMode, kLanes>;
+  using St = Stage<T, kTensors, kMode, TileT>;
   const St stage(slots);
   __shared__ uint64_t full[St::kBufs];
   const int64_t rounds = (p.tiles + size - 1) / size;
@@ -78,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
       }
     } else {
       const int64_t t0 = (k * size + rank) * TileT::kLen + first;
-      const int left = rows_left(end, t0);
+      const int left = rows_left(end, t0, kSteps);
       stage.fetch(buf, 0, gp + t0 * p.g.rs, p.g.rs, next, left);
       stage.fetch(buf, 1, vp + t0 * p.v.rs, p.v.rs, next, left);
       if constexpr (kGate) stage.fetch(buf, 2, zp + t0 * p.z.rs, p.z.rs, next, left);
@@ -123,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
       a = fmul2(a, f[i]);
       b = ffma2(f[i], b, u[i]);
     }
-    float2 s = carry_in<kLanes, false>(sh, k, make_float4(a.x, a.y, b.x, b.y), h, rank,
+    float2 s = carry_in<TileT, false>(sh, k, make_float4(a.x, a.y, b.x, b.y), h, rank,
                                        size, flags, [&] {
                                          // (the tile before this one is read: its buffer is free)
                                          if constexpr (kMode == kTma) fetch(k + St::kAhead);
@@ -166,8 +174,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3)
 
 template <typename T>
 cudaError_t scan_type(const ssmq_gated_args& a, cudaStream_t st) {
-  const Shape s = shape_for(a.batch, a.seqlen, a.dim);
-  const int len = s.narrow ? Tile<8>::kLen : Tile<32>::kLen;
+  const Shape s = shape_for<ScanTile<32>, ScanTile<8>>(a.batch, a.seqlen, a.dim,
+                                                       kScanCtas * (int64_t)sm_count(), 1);
+  const int len = s.narrow ? ScanTile<8>::kLen : ScanTile<32>::kLen;
   ScanParams p;
   p.L = a.seqlen;
   p.d = a.dim;
@@ -187,14 +196,15 @@ cudaError_t scan_type(const ssmq_gated_args& a, cudaStream_t st) {
                    pairs_ok<T>(a.y);
   const bool z = a.z.p != nullptr;
   Maps maps = {};
-  const int ch = s.narrow ? Tile<8>::kChannels : Tile<32>::kChannels;
+  const int ch = s.narrow ? ScanTile<8>::kChannels : ScanTile<32>::kChannels;
   auto map = [&](int i, const ssmq_rows& r) {
     return map_rows<T>(maps.m + i, r, a.batch, a.seqlen, a.dim, ch, len);
   };
   const int mode = !vec ? kSingle
                         : (map(0, a.g) && map(1, a.v) && (!z || map(2, a.z)) ? kTma : kPairs);
 #define SSMQ_GATED(M, N, Z)                       \
-  return launch<gated_scan_kernel<T, M, N, Z>>(p, maps, s, Stage<T, Z ? 3 : 2, M, N>::kBytes, st)
+  return launch<gated_scan_kernel<T, M, N, Z>>(p, maps, s, ScanTile<N>::kThreads, \
+                                               Stage<T, Z ? 3 : 2, M, ScanTile<N>>::kBytes, st)
 #define SSMQ_GATED_N(N)                                          \
   switch (mode) {                                                \
     case kTma: if (z) SSMQ_GATED(kTma, N, true); SSMQ_GATED(kTma, N, false);       \

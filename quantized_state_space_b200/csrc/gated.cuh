@@ -21,9 +21,6 @@
 namespace ssmq {
 namespace gated {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kSteps = 8;        // consecutive steps per thread
 constexpr int kMaxCluster = 16;  // CTAs along time (above 8: non-portable)
 constexpr uint32_t kWaitLimit = 1u << 20;
 
@@ -34,14 +31,16 @@ enum {
   kSingle = 2  // each thread its own channels one by one
 };
 
-template <int kLanes>
+template <int kWarps_, int kSteps_, int kLanes_>
 struct Tile {
+  static constexpr int kWarps = kWarps_, kSteps = kSteps_, kLanes = kLanes_;
+  static constexpr int kThreads = 32 * kWarps;
   static constexpr int kChannels = 2 * kLanes;
   static constexpr int kSubs = 32 / kLanes;  // segments per warp
   static constexpr int kLen = kWarps * kSubs * kSteps;
+  static_assert(kLen % kGatedStateSteps == 0, "saved states at tile starts");
+  static_assert(kGatedStateSteps % kSteps == 0, "saved states at segment starts");
 };
-static_assert(Tile<32>::kLen % kGatedStateSteps == 0, "saved states at tile starts");
-static_assert(kGatedStateSteps % kSteps == 0, "saved states at segment starts");
 
 struct Rows {
   void* p;
@@ -90,9 +89,9 @@ struct Maps {
 // beyond the tensor read as zero.  Otherwise every thread copies the pairs of
 // its own steps into slots of its own ([step][thread]).  Either way a thread
 // reads only its own steps and channels.
-template <typename T, int kTensors, int kMode, int kLanes>
+template <typename T, int kTensors, int kMode, typename TileT>
 struct Stage {
-  using TileT = Tile<kLanes>;
+  static constexpr int kThreads = TileT::kThreads, kSteps = TileT::kSteps;
   // (two or three CTAs' buffers fit an SM)
   static constexpr int kBufs =
       kMode == kTma ? (sizeof(T) == 2 && kTensors == 2 ? 3 : 2) : (sizeof(T) == 4 ? 1 : 2);
@@ -106,8 +105,8 @@ struct Stage {
   __device__ __forceinline__ explicit Stage(uint8_t* smem) {
     if constexpr (kMode == kTma) {
       const int lane = threadIdx.x & 31;
-      const int row = ((int)(threadIdx.x >> 5) * TileT::kSubs + lane / kLanes) * kSteps;
-      base = smem + row * kStepBytes + (lane % kLanes) * 2 * (int)sizeof(T);
+      const int row = ((int)(threadIdx.x >> 5) * TileT::kSubs + lane / TileT::kLanes) * kSteps;
+      base = smem + row * kStepBytes + (lane % TileT::kLanes) * 2 * (int)sizeof(T);
     } else {
       base = smem + threadIdx.x * 2 * (int)sizeof(T);
     }
@@ -177,10 +176,10 @@ struct Stage {
     asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
   }
 };
-// rows of the segment at t0 that lie before the end, at most kSteps
-__device__ __forceinline__ int rows_left(int64_t end, int64_t t0) {
+// rows of the segment at t0 that lie before the end, at most `steps`
+__device__ __forceinline__ int rows_left(int64_t end, int64_t t0, int steps) {
   const int64_t n = end - t0;
-  return n < 0 ? 0 : (n < kSteps ? (int)n : kSteps);
+  return n < 0 ? 0 : (n < steps ? (int)n : steps);
 }
 
 // e = exp(-g) with the exponent kept below 2^126, r = 1 / (1 + e): n = 1 - f =
@@ -254,16 +253,17 @@ __device__ __forceinline__ float4 shfl_f4(float4 v, int src) {
                      __shfl_sync(0xFFFFFFFFu, v.z, src), __shfl_sync(0xFFFFFFFFu, v.w, src));
 }
 
-template <int kLanes>
+template <typename TileT>
 struct Shared {
+  static constexpr int kWarps = TileT::kWarps, kLanes = TileT::kLanes;
   float4 warp[2][kWarps][kLanes];
   float4 cta[2][kLanes == 32 ? 8 : kMaxCluster][kLanes];  // (wide blocks: portable clusters)
   uint64_t bar[2];  // the maps of all CTAs of a round have arrived
 };
 
 // Before the first round (every thread of the cluster).
-template <int kLanes>
-__device__ __forceinline__ void carry_init(Shared<kLanes>& sh, uint32_t size) {
+template <typename TileT>
+__device__ __forceinline__ void carry_init(Shared<TileT>& sh, uint32_t size) {
   if (size == 1) return;
   if (threadIdx.x == 0) {
     tc::mbar_init(sh.bar, 1);
@@ -284,12 +284,12 @@ __device__ __forceinline__ void carry_done(uint32_t size) {
 // round k + 2 only after it has every map of round k + 1, and a CTA pushes
 // round k + 1 only when its threads are done with round k.  met() runs behind the CTA's
 // barrier: every thread is done with the rounds before this one.
-template <int kLanes, bool kReverse, typename Met>
-__device__ __forceinline__ float2 carry_in(Shared<kLanes>& sh, int64_t k, float4 m, float2& h,
+template <typename TileT, bool kReverse, typename Met>
+__device__ __forceinline__ float2 carry_in(Shared<TileT>& sh, int64_t k, float4 m, float2& h,
                                            uint32_t rank, uint32_t size, uint32_t& flags,
                                            Met met) {
   const int buf = (int)(k & 1);
-  constexpr int kSubs = 32 / kLanes;
+  constexpr int kSubs = TileT::kSubs, kLanes = TileT::kLanes, kWarps = TileT::kWarps;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub0 = lane / kLanes, l = lane % kLanes;
   const int sub = kReverse ? kSubs - 1 - sub0 : sub0;  // position in processing order
@@ -310,12 +310,12 @@ __device__ __forceinline__ float2 carry_in(Shared<kLanes>& sh, int64_t k, float4
   }
   __syncthreads();
   met();
-  float4 pre = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
-#pragma unroll 1
-  for (int i = 0; i < w; ++i) pre = compose(pre, sh.warp[buf][i][l]);
-  float4 all = pre;
-#pragma unroll 1
-  for (int i = w; i < kWarps; ++i) all = compose(all, sh.warp[buf][i][l]);
+  float4 pre = make_float4(1.0f, 1.0f, 0.0f, 0.0f), all = pre;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    if (i == w) pre = all;
+    all = compose(all, sh.warp[buf][i][l]);
+  }
   float2 base = h;
   if (size > 1) {
     // warp i tells CTA i (and i + 8) of the cluster what this CTA's tile does to a state
@@ -328,9 +328,14 @@ __device__ __forceinline__ float2 carry_in(Shared<kLanes>& sh, int64_t k, float4
       flags |= SSMQ_DEV_TIMEOUT;
     __syncwarp();
     float2 s = h;
-    for (uint32_t r = 0; r < size; ++r) {
+    // (two at a time, a power of two in all: the loads do not wait on one another)
+#pragma unroll 2
+    for (uint32_t r = 0; r < size; r += 2) {
+      const float4 m0 = sh.cta[buf][r][l], m1 = sh.cta[buf][r + 1][l];
       if (r == rank) base = s;
-      s = apply(sh.cta[buf][r][l], s);
+      s = apply(m0, s);
+      if (r + 1 == rank) base = s;
+      s = apply(m1, s);
     }
     h = s;
   } else {
@@ -346,27 +351,30 @@ struct Shape {
   unsigned grid;
   int64_t blocks;   // channel blocks per sequence
 };
-inline Shape shape_for(int64_t b, int64_t L, int64_t d) {
+// Wide and Narrow: the kernel's tiles; resident: CTAs that the GPU holds at once;
+// fills: how many times the CTAs are to fill it.
+template <typename Wide, typename Narrow>
+inline Shape shape_for(int64_t b, int64_t L, int64_t d, int64_t resident, int fills) {
   Shape s;
-  // Enough CTAs for eight per SM, first by splitting time over a cluster, then
-  // by narrower channel blocks (32-byte rows of 16-bit elements), then by
-  // clusters of 16.
-  const int64_t want = 8 * (int64_t)sm_count();
+  // Time is split over a cluster until the CTAs (nearly) fill the GPU; where that
+  // leaves most of it idle, narrower channel blocks (32-byte rows of 16-bit
+  // elements) and clusters of 16.
   auto pick = [&](int channels, int len, int most) {
     s.blocks = (d + channels - 1) / channels;
     const int64_t tiles = (L + len - 1) / len;
     s.cluster = 1;
-    while (s.cluster < most && s.cluster < tiles && b * s.blocks * s.cluster < want)
+    while (s.cluster < most && s.cluster < tiles && 
+           b * s.blocks * s.cluster < resident * fills * 85 / 100)
       s.cluster *= 2;
     return b * s.blocks * s.cluster;
   };
   s.narrow = false;
-  int64_t n = pick(Tile<32>::kChannels, Tile<32>::kLen, 8);
-  if (n < want / 4) {
+  int64_t n = pick(Wide::kChannels, Wide::kLen, 8);
+  if (n < resident * 3 / 4) {
     const Shape wide = s;
     s.narrow = true;
-    const int64_t m = pick(Tile<8>::kChannels, Tile<8>::kLen, kMaxCluster);
-    if (m <= n || L <= Tile<8>::kLen / 2) s = wide;
+    const int64_t m = pick(Narrow::kChannels, Narrow::kLen, kMaxCluster);
+    if (m <= n || L <= Narrow::kLen / 2) s = wide;
     else n = m;
   }
   s.grid = (unsigned)n;
@@ -374,14 +382,16 @@ inline Shape shape_for(int64_t b, int64_t L, int64_t d) {
 }
 
 template <auto kern, typename Params>
-cudaError_t launch(const Params& p, const Maps& maps, const Shape& s, int smem, cudaStream_t st) {
+cudaError_t launch(const Params& p, const Maps& maps, const Shape& s, int threads, int smem,
+                   cudaStream_t st) {
   static std::atomic<uint64_t> done{0}, wide{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, done);
-  if (e == cudaSuccess && s.cluster > 8) e = allow_wide_cluster(reinterpret_cast<const void*>(kern), wide);
+  if (e == cudaSuccess && s.cluster > 8)
+    e = allow_wide_cluster(reinterpret_cast<const void*>(kern), wide);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(s.grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];

@@ -19,6 +19,10 @@ namespace {
 
 using namespace gated;
 
+template <int kLanes>
+using GradTile = Tile<8, 8, kLanes>;
+constexpr int kGradCtas = 2;  // per SM
+
 struct GradParams {
   int64_t L, d, blocks;
   int64_t tiles, saved;
@@ -31,12 +35,13 @@ struct GradParams {
 };
 
 template <typename T, int kMode, int kLanes, bool kGate>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(GradTile<kLanes>::kThreads, kGradCtas)
     gated_scan_grad_kernel(const GradParams p, const __grid_constant__ Maps maps) {
   constexpr bool kVec = kMode != kSingle;
-  __shared__ Shared<kLanes> sh;
-  __shared__ float4 s_fwd[2][kWarps][kLanes];
-  using TileT = Tile<kLanes>;
+  using TileT = GradTile<kLanes>;
+  constexpr int kSteps = TileT::kSteps;
+  __shared__ Shared<TileT> sh;
+  __shared__ float4 s_fwd[2][TileT::kWarps][kLanes];
   const uint32_t size = cluster_size(), rank = cluster_rank();
   const int64_t unit = blockIdx.x / size;
   const int64_t seq = unit / p.blocks, blk = unit % p.blocks;
@@ -66,7 +71,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   extern __shared__ __align__(128) uint8_t slots[];
   constexpr int kTensors = kGate ? 4 : 3;
-  using St = Stage<T, kTensors, kMode, kLanes>;
+  using St = Stage<T, kTensors, kMode, TileT>;
   const St stage(slots);
   __shared__ uint64_t full[St::kBufs];
   const int64_t rounds = (p.tiles + size - 1) / size;
@@ -87,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     } else {
       if (k < rounds) {
         const int64_t t0 = tile >= 0 ? tile * TileT::kLen + first : 0;
-        const int left = tile >= 0 ? rows_left(end, t0) : 0;
+        const int left = tile >= 0 ? rows_left(end, t0, kSteps) : 0;
         stage.fetch(buf, 0, gp + t0 * p.g.rs, p.g.rs, next, left);
         stage.fetch(buf, 1, vp + t0 * p.v.rs, p.v.rs, next, left);
         stage.fetch(buf, 2, dyp + t0 * p.dy.rs, p.dy.rs, next, left);
@@ -116,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int64_t tile = tile_of(k);
     const bool real = tile >= 0;
     const int64_t t0 = real ? tile * TileT::kLen + first : 0;
-    const int left = real ? rows_left(end, t0) : 0;
+    const int left = real ? rows_left(end, t0, kSteps) : 0;
     if constexpr (kMode == kTma)
       if (left < kSteps) stage.clear(buf, left);
     float2 hs = make_float2(0.0f, 0.0f);  // state before the tile
@@ -171,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (sub > 0) mine = before;
       }
       // (the barrier inside carry_in orders s_fwd as well)
-      r = carry_in<kLanes, true>(sh, k, make_float4(a.x, a.y, r.x, r.y), c, rank, size, flags,
+      r = carry_in<TileT, true>(sh, k, make_float4(a.x, a.y, r.x, r.y), c, rank, size, flags,
                                  [&] {
                                    if constexpr (kMode == kTma) fetch(k + St::kAhead);
                                  });
@@ -229,8 +234,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 template <typename T>
 cudaError_t grad_type(const ssmq_gated_grad_args& a, cudaStream_t st) {
-  const Shape s = shape_for(a.batch, a.seqlen, a.dim);
-  const int len = s.narrow ? Tile<8>::kLen : Tile<32>::kLen;
+  // (four rounds of CTAs: a CTA's start and end weigh less than an idle SM)
+  const Shape s = shape_for<GradTile<32>, GradTile<8>>(a.batch, a.seqlen, a.dim,
+                                                       kGradCtas * (int64_t)sm_count(), 4);
+  const int len = s.narrow ? GradTile<8>::kLen : GradTile<32>::kLen;
   GradParams p;
   p.L = a.seqlen;
   p.d = a.dim;
@@ -254,7 +261,7 @@ cudaError_t grad_type(const ssmq_gated_grad_args& a, cudaStream_t st) {
                    pairs_ok<T>(a.dv) && pairs_ok<T>(a.dg) &&
                    (!z || (pairs_ok<T>(a.z) && pairs_ok<T>(a.dz)));
   Maps maps = {};
-  const int ch = s.narrow ? Tile<8>::kChannels : Tile<32>::kChannels;
+  const int ch = s.narrow ? GradTile<8>::kChannels : GradTile<32>::kChannels;
   auto map = [&](int i, const ssmq_rows& r) {
     return map_rows<T>(maps.m + i, r, a.batch, a.seqlen, a.dim, ch, len);
   };
@@ -263,8 +270,8 @@ cudaError_t grad_type(const ssmq_gated_grad_args& a, cudaStream_t st) {
                                ? kTma
                                : kPairs);
 #define SSMQ_GATED(M, N, Z)                                                                  \
-  return launch<gated_scan_grad_kernel<T, M, N, Z>>(p, maps, s, Stage<T, Z ? 4 : 3, M, N>::kBytes, \
-                                                    st)
+  return launch<gated_scan_grad_kernel<T, M, N, Z>>(p, maps, s, GradTile<N>::kThreads,  \
+                                                    Stage<T, Z ? 4 : 3, M, GradTile<N>>::kBytes, st)
 #define SSMQ_GATED_N(N)                                          \
   switch (mode) {                                                \
     case kTma: if (z) SSMQ_GATED(kTma, N, true); SSMQ_GATED(kTma, N, false);       \

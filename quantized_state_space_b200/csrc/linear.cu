@@ -234,14 +234,14 @@ constexpr int kMaxSplit = 8;
 template <int kTok>
 struct SplitCfg {
   static constexpr int kStage = kOperand + kTok * kBlockK;
-  static constexpr int kRed = kTok * kRows * 4;  // with a split only
+  // with a split: [part][channel][token column of the CTA], rows 16 bytes longer
+  // than their columns (no bank conflicts)
+  static int red(int split) { return split > 1 ? (kTok + 4 * split) * kRows * 4 : 0; }
   static constexpr int kBars = 256;              // barriers, TMEM address, abort word
   static constexpr int kMaxStages = 12;
   static constexpr int kCols = kTok < 32 ? 32 : kTok;
   static constexpr int kLd = kTok < 32 ? 16 : 32;  // token columns per TMEM load
-  static int smem(int stages, bool split) {
-    return 1024 + kBars + stages * kStage + (split ? kRed : 0);
-  }
+  static int smem(int stages, int split) { return 1024 + kBars + stages * kStage + red(split); }
 };
 
 template <int kTok>
@@ -333,7 +333,8 @@ __global__ void __launch_bounds__(kSplitThreads)
   }
   __syncwarp();
 
-  const int per = (kTok + split - 1) / split;  // token columns that a CTA finishes
+  const int per = kTok / split;  // token columns that a CTA finishes: a multiple of 4
+  const int pitch = per + 4;
   const int ch = (warp & 3) * 32 + lane;
   const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
   Channel c;
@@ -353,16 +354,15 @@ __global__ void __launch_bounds__(kSplitThreads)
         store_any(p, c, tok0 + j, xs, v);
         xs = next;
       } else {
-        // column j goes to CTA j / per, which keeps [part][column][channel]
-        int owner = j / per, at = j % per;
-        const uint32_t local = tc::smem_u32(red + (int)rank * per * kRows + ch);
+        // column j goes to CTA j / per
+        const uint32_t local = tc::smem_u32(red + ((int)rank * kRows + ch) * pitch);
 #pragma unroll
-        for (int i = 0; i < kLd; ++i) {
-          asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(
-                           mapa(local + (uint32_t)at * kRows * 4, (uint32_t)owner)),
-                       "r"(v[i])
+        for (int i = 0; i < kLd; i += 4) {
+          const int owner = (j + i) / per, at = (j + i) % per;
+          asm volatile("st.shared::cluster.v4.s32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           mapa(local + (uint32_t)at * 4, (uint32_t)owner)),
+                       "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3])
                        : "memory");
-          if (++at == per) at = 0, ++owner;
         }
       }
     }
@@ -370,18 +370,24 @@ __global__ void __launch_bounds__(kSplitThreads)
   if (split > 1) {
     // this CTA's columns: their scales arrive while the others finish
     const int64_t mine = tok0 + (int64_t)rank * per;
-    const int64_t left = p.M - mine;
-    int n = kTok - (int)rank * per;
-    n = n < per ? n : per;
-    n = left < n ? (int)left : n;
-    const float xs = warp < 4 ? token_scale(p, mine, per) : 0.0f;
+    float xs[kTok >= 64 ? 2 : 1];
+#pragma unroll
+    for (int i = 0; i < (kTok >= 64 ? 2 : 1); ++i)
+      xs[i] = warp < 4 ? token_scale(p, mine + 32 * i, per - 32 * i) : 0.0f;
     cluster_sync();
     if (warp < 4) {
-      for (int j = 0; j < n; ++j) {
-        int acc = 0;
-        for (int r = 0; r < split; ++r) acc += red[(r * per + j) * kRows + ch];
-        const float s = per <= 32 ? __shfl_sync(0xFFFFFFFFu, xs, j & 31) : __ldg(p.xs + mine + j);
-        store_one(p, c, mine + j, s, acc);
+#pragma unroll 1
+      for (int j = 0; j < per; j += 4) {
+        if (mine + j >= p.M) break;
+        int acc[4] = {0, 0, 0, 0};
+#pragma unroll 4
+        for (int r = 0; r < split; ++r) {
+          const int4 q = *reinterpret_cast<const int4*>(red + (r * kRows + ch) * pitch + j);
+          acc[0] += q.x, acc[1] += q.y, acc[2] += q.z, acc[3] += q.w;
+        }
+        // (the scales of columns j .. j + 3 to lanes 0 .. 3)
+        const float s = kTok >= 64 && j >= 32 ? xs[kTok >= 64 ? 1 : 0] : xs[0];
+        store_any(p, c, mine + j, __shfl_sync(0xFFFFFFFFu, s, (lane + j) & 31), acc);
       }
     }
   }
@@ -643,17 +649,18 @@ cudaError_t launch_split(const CUtensorMap& wmap, const CUtensorMap& xmap, LinPa
   if (tiles > 0x7fffffff / kMaxSplit) return cudaErrorInvalidConfiguration;
   int split = 1;
   // parts of K while the CTAs fit the SMs once and a part keeps four K blocks
-  while (split < kMaxSplit && tiles * split * 2 <= sm_count() && p.kblocks >= 8 * split)
+  while (split < kMaxSplit && split < kTok / 4 && tiles * split * 2 <= sm_count() &&
+         p.kblocks >= 8 * split)
     split *= 2;
   // One CTA per SM takes all the stages that fit (or that its K needs); several
   // share the shared memory two to an SM.
   const int room = (tiles * split <= sm_count() ? 224 : 110) * 1024;
-  int stages = (room - Cfg::smem(0, split > 1)) / Cfg::kStage;
+  int stages = (room - Cfg::smem(0, split)) / Cfg::kStage;
   const int need = (p.kblocks + split - 1) / split;
   stages = stages < Cfg::kMaxStages ? stages : Cfg::kMaxStages;
   stages = stages < need ? stages : need;
   stages = stages < 2 ? 2 : stages;
-  const int smem = Cfg::smem(stages, split > 1);
+  const int smem = Cfg::smem(stages, split);
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(int8_linear_split_kernel<kTok>),
                                    227 * 1024, done);
