@@ -640,25 +640,26 @@ def _cuda(t, name, dim=None):
     """The device and type id of a call's leading tensor."""
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if t.dtype not in _DTYPE_IDS or (dim is not None and t.dim() != dim):
+    kind = _DTYPE_IDS.get(t.dtype)
+    if kind is None or (dim is not None and t.dim() != dim):
         raise ValueError("%s must be a %sfloat16, bfloat16 or float32 tensor (got %s of %s)"
                          % (name, "" if dim is None else "%d-dimensional " % dim, t.dtype,
                             tuple(t.shape)))
-    return t.device, _DTYPE_IDS[t.dtype]
+    return t.device, kind
 
 
 def _dense(t, name, dtype, numel, device):
     """Address of a dense tensor of ``numel`` elements, 0 for None."""
     if t is None:
         return 0
-    if t.dtype != dtype or t.numel() != numel or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.numel() != numel or t.device != device or not t.is_contiguous():
         _in(t, name, dtype, numel, device)
     return t.data_ptr()
 
 
 def _status_ptr(t, device):
     _status(t, device)
-    return 0 if t is None else t.data_ptr()
+    return t.data_ptr()
 
 
 def _row_tensor(t, name, shape, dtype, device):
@@ -666,7 +667,7 @@ def _row_tensor(t, name, shape, dtype, device):
     this shape, dtype and device, its last dimension contiguous."""
     if t.device != device:
         raise ValueError("%s must be on %s" % (name, device))
-    if t.dtype != dtype or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError("%s must be %s of shape %s (got %s of %s)"
                          % (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
     if t.stride(-1) != 1 and shape[-1] > 1:
@@ -676,9 +677,10 @@ def _row_tensor(t, name, shape, dtype, device):
 def _flat_rows(t, name, shape, dtype, device):
     """(address, row stride) of a (..., d) tensor seen as (tokens, d): the
     leading dimensions must merge into one with a constant stride."""
-    _row_tensor(t, name, shape, dtype, device)
-    if t.is_contiguous():
+    if (t.dtype is dtype and t.is_contiguous() and t.shape == shape and
+            t.device == device):
         return t.data_ptr(), shape[-1]
+    _row_tensor(t, name, shape, dtype, device)
     stride, span = None, 0
     for size, st in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
         if size == 1:
@@ -714,33 +716,40 @@ def rms_norm_quantize(x, weight=None, *, residual=None, eps=1e-5, residual_out=N
     wp = _dense(weight, "weight", torch.float32, d, dv)
     rp = rs = op = os = yp = ys = qp = qs = sp = 0
     out = ()
+    # (an output that the call allocates is dense and needs no check)
     if residual is not None:
         rp, rs = _flat_rows(residual, "residual", shape, dt, dv)
         if residual_out is None:
-            residual_out = torch.empty(shape, dtype=dt, device=dv)
+            residual_out = torch.empty(*shape, dtype=dt, device=dv)
+            op, os = residual_out.data_ptr(), d
         out = (residual_out,)
-    if residual_out is not None:
+    if op == 0 and residual_out is not None:
         op, os = _flat_rows(residual_out, "residual_out", shape, dt, dv)
-    if want_y or y is not None:
-        if y is None:
-            y = torch.empty(shape, dtype=dt, device=dv)
+    if y is not None:
         yp, ys = _flat_rows(y, "y", shape, dt, dv)
+        out += (y,)
+    elif want_y:
+        y = torch.empty(*shape, dtype=dt, device=dv)
+        yp, ys = y.data_ptr(), d
         out += (y,)
     if want_codes or codes is not None or scales is not None:
         lead = shape[:-1]
-        if codes is None:
-            if d % 16:
-                codes = torch.empty((*lead, (d + 15) // 16 * 16), dtype=torch.int8,
-                                    device=dv)[..., :d]
-            else:
-                codes = torch.empty(shape, dtype=torch.int8, device=dv)
+        if codes is not None:
+            qp, qs = _flat_rows(codes, "codes", shape, torch.int8, dv)
+        elif d % 16:
+            qs = (d + 15) // 16 * 16
+            codes = torch.empty(*lead, qs, dtype=torch.int8, device=dv)[..., :d]
+            qp = codes.data_ptr()
+        else:
+            codes = torch.empty(*shape, dtype=torch.int8, device=dv)
+            qp, qs = codes.data_ptr(), d
         if scales is None:
             scales = torch.empty(lead, dtype=torch.float32, device=dv)
-        qp, qs = _flat_rows(codes, "codes", shape, torch.int8, dv)
-        _out(scales, "scales", torch.float32, tokens, dv)
+        else:
+            _out(scales, "scales", torch.float32, tokens, dv)
         sp = scales.data_ptr()
     _call(dv, N.ssmq_rms_norm_quantize, tokens, d, kind, eps, xp, xs, rp, rs, wp, op, os, yp, ys,
-          qp, qs, sp, _status_ptr(status, dv))
+          qp, qs, sp, 0 if status is None else _status_ptr(status, dv))
     return (codes, scales) + out
 
 
@@ -759,25 +768,28 @@ def int8_linear(x, x_scale, w, w_scale, *, bias=None, out=None, dtype=None, work
         dtype = out.dtype
     elif dtype is None:
         dtype = torch.float16
-    if dtype not in _DTYPE_IDS:
+    kind = _DTYPE_IDS.get(dtype)
+    if kind is None:
         raise ValueError("the output must be float16, bfloat16 or float32 (got %s)" % dtype)
     if not x.is_cuda or x.dim() < 1 or w.dim() != 2:
         raise ValueError("x (..., in_features) and w (out_features, in_features) must be CUDA "
                          "tensors")
     dv, shape = x.device, x.shape
-    K, n = shape[-1], w.shape[0]
+    *lead, K = shape
+    n = w.shape[0]
+    tokens = math.prod(lead)
     xp, xst = _flat_rows(x, "x", shape, torch.int8, dv)
     wp, wst = _flat_rows(w, "w", (n, K), torch.int8, dv)
-    tokens = x_scale.numel()
-    oshape = (*shape[:-1], n)
-    xsp = _dense(x_scale, "x_scale", torch.float32, math.prod(shape[:-1]), dv)
+    xsp = _dense(x_scale, "x_scale", torch.float32, tokens, dv)
     wsp = _dense(w_scale, "w_scale", torch.float32, n, dv)
-    bp = _dense(bias, "bias", torch.float32, n, dv)
+    bp = 0 if bias is None else _dense(bias, "bias", torch.float32, n, dv)
     if out is None:
-        out = torch.empty(oshape, dtype=dtype, device=dv)
-    yp, yst = _flat_rows(out, "out", oshape, dtype, dv)
-    f = (tokens, n, K, _DTYPE_IDS[dtype], xp, xst, xsp, wp, wst, wsp, bp, yp, yst,
-         _status_ptr(status, dv))
+        out = torch.empty(*lead, n, dtype=dtype, device=dv)
+        yp, yst = out.data_ptr(), n
+    else:
+        yp, yst = _flat_rows(out, "out", (*lead, n), dtype, dv)
+    f = (tokens, n, K, kind, xp, xst, xsp, wp, wst, wsp, bp, yp, yst,
+         0 if status is None else _status_ptr(status, dv))
     ws = wptr = 0
     if (xp | wp | xst | wst) % 16:
         ws = N.ssmq_int8_linear_workspace_size(*f)
@@ -794,17 +806,21 @@ def int8_linear(x, x_scale, w, w_scale, *, bias=None, out=None, dtype=None, work
 
 def _gated_rows(t, name, shape, dtype, device):
     """(address, batch stride, row stride) of a (b, L, d) tensor."""
-    _row_tensor(t, name, shape, dtype, device)
     st = t.stride()
+    if t.dtype is not dtype or t.shape != shape or t.device != device or st[-1] != 1:
+        _row_tensor(t, name, shape, dtype, device)
     return t.data_ptr(), st[0], st[1]
 
 
 _NONE = (0, 0, 0)
+_state_steps = None
 
 
 def _saved_states(L):
-    k = N.ssmq_gated_scan_state_steps()
-    return (L + k - 1) // k
+    global _state_steps
+    if _state_steps is None:
+        _state_steps = N.ssmq_gated_scan_state_steps()
+    return (L + _state_steps - 1) // _state_steps
 
 
 def _gated_scan(v, g, z, h0, lengths, y, h_final, states, return_state, save_states,
@@ -813,21 +829,27 @@ def _gated_scan(v, g, z, h0, lengths, y, h_final, states, return_state, save_sta
     shape, dt = v.shape, v.dtype
     b, L, d = shape
     if y is None:
-        y = torch.empty(shape, dtype=dt, device=dv)
-    if h_final is None and return_state:
-        h_final = torch.empty((b, d), dtype=torch.float32, device=dv)
-    stp = 0
-    if save_states or states is not None:
-        n = _saved_states(L)
-        if states is None:
-            states = torch.empty((b, n, d), dtype=torch.float32, device=dv)
-        stp = _dense(states, "states", torch.float32, b * n * d, dv)
+        y = torch.empty(b, L, d, dtype=dt, device=dv)
+        yr = y.data_ptr(), L * d, d
+    else:
+        yr = _gated_rows(y, "y", shape, dt, dv)
+    hp = sp = 0
+    if h_final is not None:
+        hp = _dense(h_final, "h_final", torch.float32, b * d, dv)
+    elif return_state:
+        h_final = torch.empty(b, d, dtype=torch.float32, device=dv)
+        hp = h_final.data_ptr()
+    if states is not None:
+        sp = _dense(states, "states", torch.float32, b * _saved_states(L) * d, dv)
+    elif save_states:
+        states = torch.empty(b, _saved_states(L), d, dtype=torch.float32, device=dv)
+        sp = states.data_ptr()
     _call(dv, N.ssmq_gated_scan, b, L, d, kind, *_gated_rows(v, "v", shape, dt, dv),
           *_gated_rows(g, "g", shape, dt, dv),
-          *(_NONE if z is None else _gated_rows(z, "z", shape, dt, dv)),
-          *_gated_rows(y, "y", shape, dt, dv), _dense(h0, "h0", torch.float32, b * d, dv),
-          _dense(h_final, "h_final", torch.float32, b * d, dv), stp,
-          _dense(lengths, "lengths", torch.int32, b, dv), _status_ptr(status, dv))
+          *(_NONE if z is None else _gated_rows(z, "z", shape, dt, dv)), *yr,
+          0 if h0 is None else _dense(h0, "h0", torch.float32, b * d, dv), hp, sp,
+          0 if lengths is None else _dense(lengths, "lengths", torch.int32, b, dv),
+          0 if status is None else _status_ptr(status, dv))
     return y, h_final, states
 
 
@@ -890,21 +912,35 @@ def gated_scan_backward(dy, v, g, states, *, z=None, dh_final=None, lengths=None
     if z is None and dz is not None:
         raise ValueError("dz without z")
     sp = _dense(states, "states", torch.float32, b * _saved_states(L) * d, dev)
+    rows = [*_gated_rows(v, "v", shape, dt, dev), *_gated_rows(g, "g", shape, dt, dev),
+            *(_NONE if z is None else _gated_rows(z, "z", shape, dt, dev)),
+            *_gated_rows(dy, "dy", shape, dt, dev)]
     if dv is None:
-        dv = torch.empty(shape, dtype=dt, device=dev)
+        dv = torch.empty(b, L, d, dtype=dt, device=dev)
+        rows += dv.data_ptr(), L * d, d
+    else:
+        rows += _gated_rows(dv, "dv", shape, dt, dev)
     if dg is None:
-        dg = torch.empty(shape, dtype=dt, device=dev)
-    if z is not None and dz is None:
-        dz = torch.empty(shape, dtype=dt, device=dev)
+        dg = torch.empty(b, L, d, dtype=dt, device=dev)
+        rows += dg.data_ptr(), L * d, d
+    else:
+        rows += _gated_rows(dg, "dg", shape, dt, dev)
+    if z is None:
+        rows += _NONE
+    elif dz is None:
+        dz = torch.empty(b, L, d, dtype=dt, device=dev)
+        rows += dz.data_ptr(), L * d, d
+    else:
+        rows += _gated_rows(dz, "dz", shape, dt, dev)
     if dh0 is None:
-        dh0 = torch.empty((b, d), dtype=torch.float32, device=dev)
-    rows = []
-    for t, name in ((v, "v"), (g, "g"), (z, "z"), (dy, "dy"), (dv, "dv"), (dg, "dg"), (dz, "dz")):
-        rows += _NONE if t is None else _gated_rows(t, name, shape, dt, dev)
+        dh0 = torch.empty(b, d, dtype=torch.float32, device=dev)
+        dp = dh0.data_ptr()
+    else:
+        dp = _dense(dh0, "dh0", torch.float32, b * d, dev)
     _call(dev, N.ssmq_gated_scan_backward, b, L, d, kind, *rows, sp,
-          _dense(dh_final, "dh_final", torch.float32, b * d, dev),
-          _dense(dh0, "dh0", torch.float32, b * d, dev),
-          _dense(lengths, "lengths", torch.int32, b, dev), _status_ptr(status, dev))
+          0 if dh_final is None else _dense(dh_final, "dh_final", torch.float32, b * d, dev), dp,
+          0 if lengths is None else _dense(lengths, "lengths", torch.int32, b, dev),
+          0 if status is None else _status_ptr(status, dev))
     return dv, dg, dz, dh0
 
 
@@ -915,17 +951,20 @@ def gated_update(state, v, g, *, z=None, y=None):
     dv, kind = _cuda(v, "v", 2)
     shape, dt = v.shape, v.dtype
     b, d = shape
-    if y is None:
-        y = torch.empty(shape, dtype=dt, device=dv)
     if state is None:
         raise ValueError("state is required")
+    hp = _dense(state, "state", torch.float32, b * d, dv)
     rows = []
     for t, name in ((v, "v"), (g, "g"), (z, "z"), (y, "y")):
-        if t is None:
-            rows += _NONE
+        if t is not None:
+            st = t.stride()
+            if t.dtype is not dt or t.shape != shape or t.device != dv or st[1] != 1:
+                _row_tensor(t, name, shape, dt, dv)
+            rows += t.data_ptr(), st[0], d
+        elif name == "y":
+            y = torch.empty(b, d, dtype=dt, device=dv)
+            rows += y.data_ptr(), d, d
         else:
-            _row_tensor(t, name, shape, dt, dv)
-            rows += (t.data_ptr(), t.stride(0), d)
-    _call(dv, N.ssmq_gated_update, b, 1, d, kind, *rows, 0,
-          _dense(state, "state", torch.float32, b * d, dv), 0, 0, 0)
+            rows += _NONE
+    _call(dv, N.ssmq_gated_update, b, 1, d, kind, *rows, 0, hp, 0, 0, 0)
     return y

@@ -14,12 +14,15 @@ namespace {
 
 using namespace gated;
 
-// Four warps of sixteen steps: with eight warps of eight the exchange between
-// segments weighed more than the steps (8 x 2048 x 1536 binary16, gated: 53 us
-// against 45), and with them three CTAs share an SM.
-template <int kLanes>
-using ScanTile = Tile<4, 16, kLanes>;
-constexpr int kScanCtas = 3;  // per SM
+// CTAs per SM that the registers of a mode's kernel are bounded for.
+template <typename T, int kMode>
+constexpr int kScanCtas = kMode == kTma ? 3 : (sizeof(T) == 4 ? 2 : 3);
+// A tile by TMA is fetched into the buffer of the round before the current one;
+// binary32 copied by the threads has room for one buffer.
+template <typename T, int kMode, int kLanes, bool kGate>
+using ScanStage = Stage<T, kGate ? 3 : 2, kMode, ModeTile<kMode, kLanes>,
+                        kMode == kTma ? (sizeof(T) == 2 && !kGate ? 3 : 2)
+                                      : (sizeof(T) == 2 ? 2 : 1)>;
 
 struct ScanParams {
   int64_t L, d, blocks;
@@ -34,10 +37,10 @@ struct ScanParams {
 };
 
 template <typename T, int kMode, int kLanes, bool kGate>
-__global__ void __launch_bounds__(ScanTile<kLanes>::kThreads, kScanCtas)
+__global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T, kMode>)
     gated_scan_kernel(const ScanParams p, const __grid_constant__ Maps maps) {
   constexpr bool kVec = kMode != kSingle;
-  using TileT = ScanTile<kLanes>;
+  using TileT = ModeTile<kMode, kLanes>;
   constexpr int kSteps = TileT::kSteps;
   __shared__ Shared<TileT> sh;
   const uint32_t size = cluster_size(), rank = cluster_rank();
@@ -65,7 +68,8 @@ __global__ void __launch_bounds__(ScanTile<kLanes>::kThreads, kScanCtas)
 
   extern __shared__ __align__(128) uint8_t slots[];
   constexpr int kTensors = kGate ? 3 : 2;
-  using St = Stage<T, kTensors, kMode, TileT>;
+  using St = ScanStage<T, kMode, kLanes, kGate>;
+  constexpr int kAhead = St::kBufs - 1;  // rounds fetched ahead
   const St stage(slots);
   __shared__ uint64_t full[St::kBufs];
   const int64_t rounds = (p.tiles + size - 1) / size;
@@ -99,14 +103,14 @@ __global__ void __launch_bounds__(ScanTile<kLanes>::kThreads, kScanCtas)
     __syncthreads();
   }
   carry_init(sh, size);
-  for (int k = 0; k < St::kAhead; ++k) fetch(k);
+  for (int k = 0; k < kAhead; ++k) fetch(k);
   for (int64_t k = 0; k < rounds; ++k) {
     const int buf = (int)(k % St::kBufs);
     if constexpr (kMode == kTma) {
       if (!tc::mbar_wait(full + buf, (uint32_t)(k / St::kBufs) & 1u, kWaitLimit))
         flags |= SSMQ_DEV_TIMEOUT;
     } else {
-      fetch(k + St::kAhead);
+      fetch(k + kAhead);
       St::wait();
     }
     const int64_t t0 = (k * size + rank) * TileT::kLen + first;
@@ -134,7 +138,7 @@ __global__ void __launch_bounds__(ScanTile<kLanes>::kThreads, kScanCtas)
     float2 s = carry_in<TileT, false>(sh, k, make_float4(a.x, a.y, b.x, b.y), h, rank,
                                        size, flags, [&] {
                                          // (the tile before this one is read: its buffer is free)
-                                         if constexpr (kMode == kTma) fetch(k + St::kAhead);
+                                         if constexpr (kMode == kTma) fetch(k + kAhead);
                                        });
     if (p.states && t0 < p.L && t0 % kGatedStateSteps == 0) {
       float* o = p.states + (seq * p.saved + t0 / kGatedStateSteps) * p.d + c0;
@@ -174,9 +178,8 @@ __global__ void __launch_bounds__(ScanTile<kLanes>::kThreads, kScanCtas)
 
 template <typename T>
 cudaError_t scan_type(const ssmq_gated_args& a, cudaStream_t st) {
-  const Shape s = shape_for<ScanTile<32>, ScanTile<8>>(a.batch, a.seqlen, a.dim,
-                                                       kScanCtas * (int64_t)sm_count(), 1);
-  const int len = s.narrow ? ScanTile<8>::kLen : ScanTile<32>::kLen;
+  const Shape s = shape_for(a.batch, a.seqlen, a.dim, 3 * (int64_t)sm_count(), 1);
+  const int len = s.narrow ? kNarrowLen : kWideLen;
   ScanParams p;
   p.L = a.seqlen;
   p.d = a.dim;
@@ -196,15 +199,15 @@ cudaError_t scan_type(const ssmq_gated_args& a, cudaStream_t st) {
                    pairs_ok<T>(a.y);
   const bool z = a.z.p != nullptr;
   Maps maps = {};
-  const int ch = s.narrow ? ScanTile<8>::kChannels : ScanTile<32>::kChannels;
+  const int ch = s.narrow ? kNarrowChannels : kWideChannels;
   auto map = [&](int i, const ssmq_rows& r) {
     return map_rows<T>(maps.m + i, r, a.batch, a.seqlen, a.dim, ch, len);
   };
   const int mode = !vec ? kSingle
                         : (map(0, a.g) && map(1, a.v) && (!z || map(2, a.z)) ? kTma : kPairs);
 #define SSMQ_GATED(M, N, Z)                       \
-  return launch<gated_scan_kernel<T, M, N, Z>>(p, maps, s, ScanTile<N>::kThreads, \
-                                               Stage<T, Z ? 3 : 2, M, ScanTile<N>>::kBytes, st)
+  return launch<gated_scan_kernel<T, M, N, Z>>(p, maps, s, (ModeTile<M, N>::kThreads), \
+                                               ScanStage<T, M, N, Z>::kBytes, st)
 #define SSMQ_GATED_N(N)                                          \
   switch (mode) {                                                \
     case kTma: if (z) SSMQ_GATED(kTma, N, true); SSMQ_GATED(kTma, N, false);       \

@@ -42,6 +42,15 @@ struct Tile {
   static_assert(kGatedStateSteps % kSteps == 0, "saved states at segment starts");
 };
 
+// The tile of a mode.  With TMA four warps of sixteen steps: the exchange between
+// segments is per thread, and eight warps of eight steps spend more on it than on
+// the steps (forward, 8 x 2048 x 1536 binary16, gated: 53 us against 45; gradient,
+// 4 x 4096 x 5120 bfloat16: 264 against 250).  Where the threads copy for
+// themselves, eight warps of eight: twice the threads have copies in flight
+// (gradient, 5 x 1023 x 333 binary32: 31 us against 20).
+template <int kMode, int kLanes>
+using ModeTile = Tile<kMode == kTma ? 4 : 8, kMode == kTma ? 16 : 8, kLanes>;
+
 struct Rows {
   void* p;
   int64_t bs, rs;
@@ -89,14 +98,10 @@ struct Maps {
 // beyond the tensor read as zero.  Otherwise every thread copies the pairs of
 // its own steps into slots of its own ([step][thread]).  Either way a thread
 // reads only its own steps and channels.
-template <typename T, int kTensors, int kMode, typename TileT>
+template <typename T, int kTensors, int kMode, typename TileT, int kBufs_>
 struct Stage {
   static constexpr int kThreads = TileT::kThreads, kSteps = TileT::kSteps;
-  // (two or three CTAs' buffers fit an SM)
-  static constexpr int kBufs =
-      kMode == kTma ? (sizeof(T) == 2 && kTensors == 2 ? 3 : 2) : (sizeof(T) == 4 ? 1 : 2);
-  static_assert(kMode != kTma || kBufs > 1, "a tile is fetched while another is read");
-  static constexpr int kAhead = kBufs > 1 ? kBufs - 1 : 0;  // rounds fetched ahead
+  static constexpr int kBufs = kBufs_;
   static constexpr int kTensorBytes = TileT::kLen * TileT::kChannels * (int)sizeof(T);
   static constexpr int kStepBytes =
       (kMode == kTma ? TileT::kChannels : 2 * kThreads) * (int)sizeof(T);
@@ -171,9 +176,9 @@ struct Stage {
   static __device__ __forceinline__ void commit() {
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  // all but the newest kAhead groups have landed
+  // all but the newest kBufs - 1 groups have landed
   static __device__ __forceinline__ void wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(kBufs - 1) : "memory");
   }
 };
 // rows of the segment at t0 that lie before the end, at most `steps`
@@ -236,6 +241,22 @@ __device__ __forceinline__ void push_f4(float4* local, uint64_t* bar, uint32_t r
       "[%5];" ::"r"(a),
       "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(b)
       : "memory");
+}
+
+// tc::mbar_wait, acquiring what the other CTAs of the cluster wrote
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity), "r"(1000u)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
 }
 
 // (A, B) of two channels: {A0, A1, B0, B1}; h -> A h + B
@@ -324,7 +345,7 @@ __device__ __forceinline__ float2 carry_in(Shared<TileT>& sh, int64_t k, float4 
     if (sub0 == 0)
       for (uint32_t r = (uint32_t)warp; r < size; r += kWarps)
         push_f4(&sh.cta[buf][rank][l], sh.bar + buf, r, all);
-    if (!tc::mbar_wait(sh.bar + buf, (uint32_t)(k >> 1) & 1u, kWaitLimit))
+    if (!wait_cluster(sh.bar + buf, (uint32_t)(k >> 1) & 1u))
       flags |= SSMQ_DEV_TIMEOUT;
     __syncwarp();
     float2 s = h;
@@ -351,30 +372,34 @@ struct Shape {
   unsigned grid;
   int64_t blocks;   // channel blocks per sequence
 };
-// Wide and Narrow: the kernel's tiles; resident: CTAs that the GPU holds at once;
-// fills: how many times the CTAs are to fill it.
-template <typename Wide, typename Narrow>
+// (the tiles of all modes have the same sizes)
+constexpr int kWideChannels = ModeTile<kTma, 32>::kChannels, kWideLen = ModeTile<kTma, 32>::kLen;
+constexpr int kNarrowChannels = ModeTile<kTma, 8>::kChannels, kNarrowLen = ModeTile<kTma, 8>::kLen;
+static_assert(ModeTile<kPairs, 32>::kLen == kWideLen && ModeTile<kPairs, 8>::kLen == kNarrowLen,
+              "tiles");
+// resident: CTAs that the GPU holds at once; fills: how many times the CTAs are to
+// fill it (nearly: 0.85).
 inline Shape shape_for(int64_t b, int64_t L, int64_t d, int64_t resident, int fills) {
   Shape s;
-  // Time is split over a cluster until the CTAs (nearly) fill the GPU; where that
-  // leaves most of it idle, narrower channel blocks (32-byte rows of 16-bit
+  // Time is split over a cluster until there are CTAs enough; where that leaves
+  // the GPU partly idle, narrower channel blocks (32-byte rows of 16-bit
   // elements) and clusters of 16.
   auto pick = [&](int channels, int len, int most) {
     s.blocks = (d + channels - 1) / channels;
     const int64_t tiles = (L + len - 1) / len;
     s.cluster = 1;
-    while (s.cluster < most && s.cluster < tiles && 
+    while (s.cluster < most && s.cluster < tiles &&
            b * s.blocks * s.cluster < resident * fills * 85 / 100)
       s.cluster *= 2;
     return b * s.blocks * s.cluster;
   };
   s.narrow = false;
-  int64_t n = pick(Wide::kChannels, Wide::kLen, 8);
-  if (n < resident * 3 / 4) {
+  int64_t n = pick(kWideChannels, kWideLen, 8);
+  if (n < resident) {
     const Shape wide = s;
     s.narrow = true;
-    const int64_t m = pick(Narrow::kChannels, Narrow::kLen, kMaxCluster);
-    if (m <= n || L <= Narrow::kLen / 2) s = wide;
+    const int64_t m = pick(kNarrowChannels, kNarrowLen, kMaxCluster);
+    if (m <= n || L <= kNarrowLen / 2) s = wide;
     else n = m;
   }
   s.grid = (unsigned)n;
@@ -414,21 +439,19 @@ bool pairs_ok(const ssmq_rows& r) {
 template <typename T>
 bool map_rows(CUtensorMap* map, const ssmq_rows& r, int64_t b, int64_t L, int64_t d, int channels,
               int len) {
-  const EncodeFn fn = tensor_map_encoder();
   const int64_t rs = (L > 1 ? r.row_stride : (d + 7) / 8 * 8) * (int64_t)sizeof(T);
   const int64_t bs = b > 1 ? r.batch_stride * (int64_t)sizeof(T) : rs * L;
   const int64_t most = (int64_t)1 << 40;
-  if (!fn || (reinterpret_cast<uintptr_t>(r.p) & 15u) || rs % 16 || bs % 16 || rs <= 0 ||
+  if ((reinterpret_cast<uintptr_t>(r.p) & 15u) || rs % 16 || bs % 16 || rs <= 0 ||
       bs <= 0 || rs >= most || bs >= most || L >= ((int64_t)1 << 31) - 65536)
     return false;
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)L, (cuuint64_t)b};
   const cuuint64_t strides[2] = {(cuuint64_t)rs, (cuuint64_t)bs};
   const cuuint32_t box[3] = {(cuuint32_t)channels, (cuuint32_t)len, 1};
-  const cuuint32_t one[3] = {1, 1, 1};
-  return fn(map, sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3,
-            r.p, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_tiled(map, sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32
+                                          : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+                      3, r.p, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_128B) == cudaSuccess;
 }
 
 }  // namespace gated

@@ -19,9 +19,10 @@ namespace {
 
 using namespace gated;
 
-template <int kLanes>
-using GradTile = Tile<8, 8, kLanes>;
 constexpr int kGradCtas = 2;  // per SM
+// A round's inputs are read before its exchange: the slot refills behind it.
+template <typename T, int kMode, int kLanes, bool kGate>
+using GradStage = Stage<T, kGate ? 4 : 3, kMode, ModeTile<kMode, kLanes>, sizeof(T) == 2 ? 2 : 1>;
 
 struct GradParams {
   int64_t L, d, blocks;
@@ -35,10 +36,10 @@ struct GradParams {
 };
 
 template <typename T, int kMode, int kLanes, bool kGate>
-__global__ void __launch_bounds__(GradTile<kLanes>::kThreads, kGradCtas)
+__global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kGradCtas)
     gated_scan_grad_kernel(const GradParams p, const __grid_constant__ Maps maps) {
   constexpr bool kVec = kMode != kSingle;
-  using TileT = GradTile<kLanes>;
+  using TileT = ModeTile<kMode, kLanes>;
   constexpr int kSteps = TileT::kSteps;
   __shared__ Shared<TileT> sh;
   __shared__ float4 s_fwd[2][TileT::kWarps][kLanes];
@@ -70,8 +71,7 @@ __global__ void __launch_bounds__(GradTile<kLanes>::kThreads, kGradCtas)
     c = make_float2(p.dh_final[seq * p.d + c0], p.dh_final[seq * p.d + c0 + next]);
 
   extern __shared__ __align__(128) uint8_t slots[];
-  constexpr int kTensors = kGate ? 4 : 3;
-  using St = Stage<T, kTensors, kMode, TileT>;
+  using St = GradStage<T, kMode, kLanes, kGate>;
   const St stage(slots);
   __shared__ uint64_t full[St::kBufs];
   const int64_t rounds = (p.tiles + size - 1) / size;
@@ -84,9 +84,9 @@ __global__ void __launch_bounds__(GradTile<kLanes>::kThreads, kGradCtas)
     if constexpr (kMode == kTma) {
       if (threadIdx.x == 0 && k < rounds && tile >= 0) {
         const int c = (int)(blk * TileT::kChannels), t = (int)(tile * TileT::kLen);
-        stream::expect_tx(full + buf, kTensors * St::kTensorBytes);
+        stream::expect_tx(full + buf, (kGate ? 4 : 3) * St::kTensorBytes);
 #pragma unroll
-        for (int i = 0; i < kTensors; ++i)
+        for (int i = 0; i < (kGate ? 4 : 3); ++i)
           St::fetch_tile(slots, buf, i, maps.m + i, c, t, (int)seq, full + buf);
       }
     } else {
@@ -107,37 +107,31 @@ __global__ void __launch_bounds__(GradTile<kLanes>::kThreads, kGradCtas)
     __syncthreads();
   }
   carry_init(sh, size);
-  for (int k = 0; k < St::kAhead; ++k) fetch(k);
+  for (int k = 0; k < St::kBufs; ++k) fetch(k);
   for (int64_t k = 0; k < rounds; ++k) {
     const int buf = (int)(k % St::kBufs);
-    if constexpr (kMode == kTma) {
-      if (tile_of(k) >= 0 &&
-          !tc::mbar_wait(full + buf, (uint32_t)(k / St::kBufs) & 1u, kWaitLimit))
-        flags |= SSMQ_DEV_TIMEOUT;
-    } else {
-      fetch(k + St::kAhead);
-      St::wait();
-    }
     const int64_t tile = tile_of(k);
     const bool real = tile >= 0;
     const int64_t t0 = real ? tile * TileT::kLen + first : 0;
     const int left = real ? rows_left(end, t0, kSteps) : 0;
-    if constexpr (kMode == kTma)
-      if (left < kSteps) stage.clear(buf, left);
     float2 hs = make_float2(0.0f, 0.0f);  // state before the tile
     if (real) {
       const float* sp = p.states +
                         (seq * p.saved + tile * (TileT::kLen / kGatedStateSteps)) * p.d + c0;
       hs = make_float2(sp[0], sp[next]);
     }
-
-    // f and n of a step; f = 1, n = 0 behind the end
-    float2 f[kSteps], n[kSteps], sg[kSteps];
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      gate2(stage.get(buf, 0, i), f[i], n[i]);
-      if constexpr (kGate) sg[i] = sigmoid2(stage.get(buf, 3, i));
+    if constexpr (kMode == kTma) {
+      if (real && !tc::mbar_wait(full + buf, (uint32_t)(k / St::kBufs) & 1u, kWaitLimit))
+        flags |= SSMQ_DEV_TIMEOUT;
+      if (left < kSteps) stage.clear(buf, left);
+    } else {
+      St::wait();
     }
+
+    // Gates and the segment's forward map h -> a h + b.  f = 1, n = 0 behind the end.
+    float2 f[kSteps], n[kSteps], q[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) gate2(stage.get(buf, 0, i), f[i], n[i]);
     if (left < kSteps) {
 #pragma unroll
       for (int i = 0; i < kSteps; ++i)
@@ -146,21 +140,14 @@ __global__ void __launch_bounds__(GradTile<kLanes>::kThreads, kGradCtas)
           n[i] = make_float2(0.0f, 0.0f);
         }
     }
-    auto dh = [&](int i) {  // dy silu(z)
-      const float2 d = stage.get(buf, 2, i);
-      if constexpr (kGate) return fmul2(d, fmul2(stage.get(buf, 3, i), sg[i]));
-      return d;
-    };
-    float2 a = f[0], b = fmul2(n[0], stage.get(buf, 1, 0)), r = make_float2(0.0f, 0.0f);
+    float2 a = f[0], b = fmul2(n[0], stage.get(buf, 1, 0));
 #pragma unroll
     for (int i = 1; i < kSteps; ++i) {
       a = fmul2(a, f[i]);
       b = ffma2(f[i], b, fmul2(n[i], stage.get(buf, 1, i)));
     }
-#pragma unroll
-    for (int i = kSteps - 1; i >= 0; --i) r = fmul2(f[i], fadd2(dh(i), r));
-
-    // forward state before this thread's segment: maps of the CTA's earlier segments
+    // Forward state before this segment: the saved state through the CTA's earlier
+    // segments.
     {
       float4 m = make_float4(a.x, a.y, b.x, b.y);
       constexpr int kSubs = TileT::kSubs;
@@ -175,45 +162,62 @@ __global__ void __launch_bounds__(GradTile<kLanes>::kThreads, kGradCtas)
         const float4 before = shfl_f4(m, (lane - kLanes) & 31);
         if (sub > 0) mine = before;
       }
-      // (the barrier inside carry_in orders s_fwd as well)
-      r = carry_in<TileT, true>(sh, k, make_float4(a.x, a.y, r.x, r.y), c, rank, size, flags,
-                                 [&] {
-                                   if constexpr (kMode == kTma) fetch(k + St::kAhead);
-                                 });
-#pragma unroll 1
-      for (int w = 0; w < warp; ++w) hs = apply(s_fwd[k & 1][w][l], hs);
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < TileT::kWarps - 1; ++w) {
+        const float4 e = s_fwd[k & 1][w][l];
+        if (w < warp) hs = apply(e, hs);
+      }
       hs = apply(mine, hs);
     }
-
-    float2 hb[kSteps];  // h_{t-1}
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      hb[i] = hs;
-      hs = ffma2(f[i], hs, fmul2(n[i], stage.get(buf, 1, i)));
-    }
-    T* dvo = dvp + t0 * p.dv.rs;
-    T* dgo = dgp + t0 * p.dg.rs;
+    // Forward through the segment.  What the gradients need of it is kept as
+    // q_t = f_t (h_{t-1} - v_t) and dh_t = dy_t silu(z_t); dz is written here.
+    float2 dh[kSteps];
     T* dzo = kGate ? dzp + t0 * p.dz.rs : nullptr;
+    auto walk = [&](int i, bool live, bool row) {
+      const float2 v = stage.get(buf, 1, i), one = make_float2(1.0f, 1.0f);
+      q[i] = fmul2(f[i], fsub2(hs, v));
+      hs = ffma2(f[i], hs, fmul2(n[i], v));
+      dh[i] = stage.get(buf, 2, i);
+      if constexpr (kGate) {
+        const float2 z = stage.get(buf, 3, i), s = sigmoid2(z);
+        // silu'(z) = s (1 + z (1 - s))
+        float2 dz = fmul2(fmul2(dh[i], hs), fmul2(s, ffma2(z, fsub2(one, s), one)));
+        dh[i] = fmul2(dh[i], fmul2(z, s));
+        if (!live) dz = make_float2(0.0f, 0.0f);
+        if (row) store_pair<T, kVec>(dzo, next, dz, in0, in1);
+        dzo += p.dz.rs;
+      }
+    };
+    if (left >= kSteps) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) walk(i, true, true);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) walk(i, i < left, real && t0 + i < p.L);
+    }
+    // The segment's backward map c -> a c + r, and the c behind the segment.
+    float2 r = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = kSteps - 1; i >= 0; --i) r = fmul2(f[i], fadd2(dh[i], r));
+    r = carry_in<TileT, true>(sh, k, make_float4(a.x, a.y, r.x, r.y), c, rank, size, flags, [&] {
+      fetch(k + St::kBufs);  // (every thread has read this round's tile)
+    });
+    T* dvo = dvp + (t0 + kSteps - 1) * p.dv.rs;
+    T* dgo = dgp + (t0 + kSteps - 1) * p.dg.rs;
     // gradients of step i, from the last step backwards
     auto put = [&](int i, bool live, bool row) {
-      const float2 lam = fadd2(dh(i), r);
+      const float2 lam = fadd2(dh[i], r);
       r = fmul2(f[i], lam);
       float2 dv = fmul2(n[i], lam);
-      float2 dg = fmul2(dv, fmul2(f[i], fsub2(hb[i], stage.get(buf, 1, i))));
+      float2 dg = fmul2(dv, q[i]);
       if (!live) dv = dg = make_float2(0.0f, 0.0f);
       if (row) {
-        store_pair<T, kVec>(dvo + i * p.dv.rs, next, dv, in0, in1);
-        store_pair<T, kVec>(dgo + i * p.dg.rs, next, dg, in0, in1);
+        store_pair<T, kVec>(dvo, next, dv, in0, in1);
+        store_pair<T, kVec>(dgo, next, dg, in0, in1);
       }
-      if constexpr (kGate) {
-        // silu'(z) = s (1 + z (1 - s))
-        const float2 z = stage.get(buf, 3, i), one = make_float2(1.0f, 1.0f);
-        const float2 h = i + 1 < kSteps ? hb[i + 1 < kSteps ? i + 1 : i] : hs;
-        const float2 ds = fmul2(sg[i], ffma2(z, fsub2(one, sg[i]), one));
-        float2 dz = fmul2(fmul2(stage.get(buf, 2, i), h), ds);
-        if (!live) dz = make_float2(0.0f, 0.0f);
-        if (row) store_pair<T, kVec>(dzo + i * p.dz.rs, next, dz, in0, in1);
-      }
+      dvo -= p.dv.rs;
+      dgo -= p.dg.rs;
     };
     if (left >= kSteps) {
 #pragma unroll
@@ -235,9 +239,8 @@ __global__ void __launch_bounds__(GradTile<kLanes>::kThreads, kGradCtas)
 template <typename T>
 cudaError_t grad_type(const ssmq_gated_grad_args& a, cudaStream_t st) {
   // (four rounds of CTAs: a CTA's start and end weigh less than an idle SM)
-  const Shape s = shape_for<GradTile<32>, GradTile<8>>(a.batch, a.seqlen, a.dim,
-                                                       kGradCtas * (int64_t)sm_count(), 4);
-  const int len = s.narrow ? GradTile<8>::kLen : GradTile<32>::kLen;
+  const Shape s = shape_for(a.batch, a.seqlen, a.dim, kGradCtas * (int64_t)sm_count(), 4);
+  const int len = s.narrow ? kNarrowLen : kWideLen;
   GradParams p;
   p.L = a.seqlen;
   p.d = a.dim;
@@ -261,7 +264,7 @@ cudaError_t grad_type(const ssmq_gated_grad_args& a, cudaStream_t st) {
                    pairs_ok<T>(a.dv) && pairs_ok<T>(a.dg) &&
                    (!z || (pairs_ok<T>(a.z) && pairs_ok<T>(a.dz)));
   Maps maps = {};
-  const int ch = s.narrow ? GradTile<8>::kChannels : GradTile<32>::kChannels;
+  const int ch = s.narrow ? kNarrowChannels : kWideChannels;
   auto map = [&](int i, const ssmq_rows& r) {
     return map_rows<T>(maps.m + i, r, a.batch, a.seqlen, a.dim, ch, len);
   };
@@ -270,8 +273,8 @@ cudaError_t grad_type(const ssmq_gated_grad_args& a, cudaStream_t st) {
                                ? kTma
                                : kPairs);
 #define SSMQ_GATED(M, N, Z)                                                                  \
-  return launch<gated_scan_grad_kernel<T, M, N, Z>>(p, maps, s, GradTile<N>::kThreads,  \
-                                                    Stage<T, Z ? 4 : 3, M, GradTile<N>>::kBytes, st)
+  return launch<gated_scan_grad_kernel<T, M, N, Z>>(p, maps, s, (ModeTile<M, N>::kThreads),  \
+                                                    GradStage<T, M, N, Z>::kBytes, st)
 #define SSMQ_GATED_N(N)                                          \
   switch (mode) {                                                \
     case kTma: if (z) SSMQ_GATED(kTma, N, true); SSMQ_GATED(kTma, N, false);       \

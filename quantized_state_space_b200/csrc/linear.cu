@@ -625,18 +625,12 @@ bool tma_rows(const void* p, int64_t rows, int64_t stride) {
 
 cudaError_t encode(CUtensorMap* map, const void* p, int64_t rows, int64_t k, int64_t stride,
                    int box_rows) {
-  const EncodeFn fn = tensor_map_encoder();
-  if (!fn) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows};
   // (one row: its stride is never used, but has to be a multiple of 16)
   const cuuint64_t strides[1] = {(cuuint64_t)(rows <= 1 ? pitch_of(k) : stride)};
   const cuuint32_t box[2] = {(cuuint32_t)kBlockK, (cuuint32_t)box_rows};
-  const cuuint32_t one[2] = {1, 1};
-  const CUresult r =
-      fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, box, one,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p, dims, strides, box,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 template <int kTok>

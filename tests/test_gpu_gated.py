@@ -360,6 +360,26 @@ def test_repeatable_streams_and_graph():
         assert torch.equal(a, b) and torch.equal(a, c) and torch.equal(a, e)
 
 
+def test_first_call_of_a_thread():
+    """A thread that has made no CUDA call yet gets the same bytes: the same
+    kernels run (tensor maps need the thread's context)."""
+    import threading
+    p = problem(21, 2, 700, 64, F16, strided=False)
+    q = torch.randint(-127, 128, (300, 256), dtype=torch.int8, device=dev())
+    s = torch.rand(300, device=dev())
+    calls = [lambda: api.gated_scan(p["v"], p["g"], z=p["z"], h0=p["h0"]),
+             lambda: [api.int8_linear(q, s, q, s)],
+             lambda: api.rms_norm_quantize(p["v"])]
+    for call in calls:
+        ref, got = call(), []
+        torch.cuda.synchronize()
+        t = threading.Thread(target=lambda: got.extend(call()))
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert len(got) == len(ref) and all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
 def test_offsets_past_32_bits():
     """Rows more than 2^32 elements from the base (a long projection buffer)."""
     L, d = 70, 16
