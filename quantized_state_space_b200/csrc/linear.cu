@@ -41,6 +41,7 @@ struct LinParams {
   int dtype;
   uint32_t* status;
   int64_t tok_tiles, ch_tiles, group;  // persistent kernel: tile order
+  bool tma_out;                        // and whether y goes out by TMA
 };
 
 // ---- PTX ---------------------------------------------------------------------
@@ -210,16 +211,28 @@ __device__ __forceinline__ void store_any(const LinParams& p, const Channel& c, 
   else
     store_tokens<float>(p, c, t0, xs, acc);
 }
-__device__ __forceinline__ void store_one(const LinParams& p, const Channel& c, int64_t t, float xs,
-                                          int acc) {
-  if (!c.in) return;
-  const float v = fmaf((float)acc, xs * c.scale, c.bias);
-  if (p.dtype == SSMQ_F16)
-    static_cast<__half*>(p.y)[t * p.ldy + c.n] = __float2half_rn(v);
-  else if (p.dtype == SSMQ_BF16)
-    static_cast<__nv_bfloat16*>(p.y)[t * p.ldy + c.n] = __float2bfloat16_rn(v);
-  else
-    static_cast<float*>(p.y)[t * p.ldy + c.n] = v;
+// The same values into a shared-memory tile [token][128 channels], at this lane's
+// channel.
+template <typename T>
+__device__ __forceinline__ void stage_tokens(const Channel& c, float xs, const int (&acc)[32],
+                                             void* at) {
+  T* o = static_cast<T*>(at);
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    o[i * kRows] = from_f32<T>(
+        fmaf((float)acc[i], __shfl_sync(0xFFFFFFFFu, xs, i) * c.scale, c.bias));
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, int ch, int tok) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   map),
+               "r"(ch), "r"(tok), "r"(src)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// shared memory of all but the newest kPending stores may be written again
+template <int kPending>
+__device__ __forceinline__ void tma_stores_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPending) : "memory");
 }
 
 // ---- few tokens: 128 channels x kTok tokens per cluster, K split over its CTAs --
@@ -402,13 +415,18 @@ __global__ void __launch_bounds__(kSplitThreads)
 // each brings 128 channels and 128 tokens per K block (half the operand
 // traffic per MMA of two separate 128 x 256 tiles), the leader issues the
 // MMAs of both.  Accumulators are double-buffered in TMEM (2 x 256 columns),
-// so eight warps per CTA write tile i while the MMAs of tile i + 1 run (four were
+// so eight warps per CTA write tile i (through shared memory by TMA, 256-byte rows,
+// where y lies on 16-byte rows) while the MMAs of tile i + 1 run (four were
 // slower than the MMAs: 206 against 126 us of MMAs at 16384 x 2560 x 5120).
 constexpr int kPairThreads = 384;  // warp 0 TMA, 1 MMA, 2 TMEM, 4-11 epilogue
 constexpr int kPairStages = 6;
 constexpr int kPairStage = 2 * kOperand;
 constexpr int kPairTok = 256, kPairCh = 256;
-constexpr int kPairSmem = 1024 + kPairStages * kPairStage + 256;
+// epilogue staging per half tile (128 channels): 32 tokens of 16 bits, twice, or of
+// 32 bits, once
+constexpr int kHalfStage = 2 * 32 * kRows * 2;
+constexpr int kPairSmem = 1024 + kPairStages * kPairStage + 2 * kHalfStage + 256;
+static_assert(kPairSmem <= 227 * 1024, "shared memory");
 
 // Tile i -> (channel tile, token tile): channels fastest inside a group of
 // p.group channel tiles, so that the tiles in flight share tokens and the
@@ -424,10 +442,12 @@ __device__ __forceinline__ void tile_at(const LinParams& p, int64_t i, int64_t& 
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
     int8_linear_pair_kernel(const __grid_constant__ CUtensorMap wmap,
-                            const __grid_constant__ CUtensorMap xmap, const LinParams p) {
+                            const __grid_constant__ CUtensorMap xmap,
+                            const __grid_constant__ CUtensorMap ymap, const LinParams p) {
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~1023ull);
-  uint64_t* full = reinterpret_cast<uint64_t*>(base + kPairStages * kPairStage);
+  uint8_t* out = base + kPairStages * kPairStage;  // epilogue staging
+  uint64_t* full = reinterpret_cast<uint64_t*>(out + 2 * kHalfStage);
   uint64_t* empty = full + kPairStages;
   uint64_t* acc_full = empty + kPairStages;  // [2]
   uint64_t* acc_empty = acc_full + 2;        // [2], the leader's collect both CTAs
@@ -553,9 +573,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
           __syncwarp();
           if (lane == 0) arrive_remote(mapa(tc::smem_u32(acc_empty + b), 0));
         }
-        if (t0 + 32 * q < p.M) store_any(p, c, t0 + 32 * q, xs[q], v[q & 1]);
+        if (t0 + 32 * q >= p.M) continue;  // (the same in the four warps of a half)
+        if (!p.tma_out) {
+          store_any(p, c, t0 + 32 * q, xs[q], v[q & 1]);
+          continue;
+        }
+        const bool wide = p.dtype == SSMQ_F32;
+        uint8_t* buf = out + (warp - 4) / 4 * kHalfStage + (wide ? 0 : (q & 1) * (kHalfStage / 2));
+        const bool one = quarter == 0 && lane == 0;  // issues the half's stores
+        if (one) {
+          if (wide)
+            tma_stores_read<0>();
+          else
+            tma_stores_read<1>();
+        }
+        tc::named_sync(1 + (warp - 4) / 4, 128);
+        const int col = quarter * 32 + lane;
+        if (wide)
+          stage_tokens<float>(c, xs[q], v[q & 1], buf + col * 4);
+        else if (p.dtype == SSMQ_F16)
+          stage_tokens<__half>(c, xs[q], v[q & 1], buf + col * 2);
+        else
+          stage_tokens<__nv_bfloat16>(c, xs[q], v[q & 1], buf + col * 2);
+        tc::fence_async_smem();
+        tc::named_sync(1 + (warp - 4) / 4, 128);
+        const int64_t ch0 = ch * kPairCh + rank * kRows;
+        if (one && ch0 < p.N) tma_store(&ymap, tc::smem_u32(buf), (int)ch0, (int)(t0 + 32 * q));
       }
     }
+    if (quarter == 0 && lane == 0)  // the stores are done before the CTA leaves
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncwarp();
   tc::fence_before();
@@ -745,8 +792,21 @@ cudaError_t launch_int8_linear(const ssmq_linear_args& a, void* ws, cudaStream_t
   static std::atomic<uint64_t> done{0};
   e = allow_smem(reinterpret_cast<const void*>(int8_linear_pair_kernel), kPairSmem, done);
   if (e != cudaSuccess) return e;
+  CUtensorMap ymap = {};
+  const int esz = p.dtype == SSMQ_F32 ? 4 : 2;
+  if (rows16(p.y, p.ldy, esz) && p.ldy < ((int64_t)1 << 36)) {
+    const cuuint64_t dims[2] = {(cuuint64_t)p.N, (cuuint64_t)p.M};
+    const cuuint64_t strides[1] = {(cuuint64_t)p.ldy * esz};
+    const cuuint32_t box[2] = {(cuuint32_t)kRows, 32};
+    p.tma_out = encode_tiled(&ymap,
+                             esz == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32
+                                      : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+                             2, p.y, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE,
+                             CU_TENSOR_MAP_L2_PROMOTION_NONE) == cudaSuccess;
+  }
   const int64_t pairs = pair_tiles < sms / 2 ? pair_tiles : sms / 2;
-  int8_linear_pair_kernel<<<(unsigned)(2 * pairs), kPairThreads, kPairSmem, st>>>(wmap, xmap, p);
+  int8_linear_pair_kernel<<<(unsigned)(2 * pairs), kPairThreads, kPairSmem, st>>>(wmap, xmap, ymap,
+                                                                                  p);
   return cudaGetLastError();
 }
 
