@@ -215,12 +215,19 @@ __device__ __forceinline__ void store_any(const LinParams& p, const Channel& c, 
 // channel.
 template <typename T>
 __device__ __forceinline__ void stage_tokens(const Channel& c, float xs, const int (&acc)[32],
-                                             void* at) {
-  T* o = static_cast<T*>(at);
+                                             uint32_t at) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i)
-    o[i * kRows] = from_f32<T>(
-        fmaf((float)acc[i], __shfl_sync(0xFFFFFFFFu, xs, i) * c.scale, c.bias));
+  for (int i = 0; i < 32; ++i) {
+    const float v = fmaf((float)acc[i], __shfl_sync(0xFFFFFFFFu, xs, i) * c.scale, c.bias);
+    if constexpr (sizeof(T) == 4) {
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + i * kRows * 4), "f"(v) : "memory");
+    } else {
+      const T h = from_f32<T>(v);
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + i * kRows * 2),
+                   "h"(*reinterpret_cast<const uint16_t*>(&h))
+                   : "memory");
+    }
+  }
 }
 __device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, int ch, int tok) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
@@ -229,10 +236,9 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, 
                : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
-// shared memory of all but the newest kPending stores may be written again
-template <int kPending>
+// the shared memory of the stores so far may be written again
 __device__ __forceinline__ void tma_stores_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPending) : "memory");
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 // ---- few tokens: 128 channels x kTok tokens per cluster, K split over its CTAs --
@@ -419,12 +425,12 @@ __global__ void __launch_bounds__(kSplitThreads)
 // where y lies on 16-byte rows) while the MMAs of tile i + 1 run (four were
 // slower than the MMAs: 206 against 126 us of MMAs at 16384 x 2560 x 5120).
 constexpr int kPairThreads = 384;  // warp 0 TMA, 1 MMA, 2 TMEM, 4-11 epilogue
-constexpr int kPairStages = 6;
+constexpr int kPairStages = 5;  // (4 to 7 measured the same)
 constexpr int kPairStage = 2 * kOperand;
 constexpr int kPairTok = 256, kPairCh = 256;
-// epilogue staging per half tile (128 channels): 32 tokens of 16 bits, twice, or of
-// 32 bits, once
-constexpr int kHalfStage = 2 * 32 * kRows * 2;
+// epilogue staging per half tile: 128 channels of 128 tokens in 16 bits, or of 64
+// in 32 bits
+constexpr int kHalfStage = 128 * kRows * 2;
 constexpr int kPairSmem = 1024 + kPairStages * kPairStage + 2 * kHalfStage + 256;
 static_assert(kPairSmem <= 227 * 1024, "shared memory");
 
@@ -561,6 +567,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
       }
       tc::fence_after();
       const uint32_t src = tmem + (uint32_t)(b * kPairTok + half) + ((uint32_t)(quarter * 32) << 16);
+      const uint32_t at = tc::smem_u32(out + (warp - 4) / 4 * kHalfStage);
+      const bool one = quarter == 0 && lane == 0;  // issues the half's stores
+      const int64_t ch0 = ch * kPairCh + rank * kRows;
+      // the half's four warps meet: its staging is free, or (after) complete
+      auto free_stage = [&] {
+        if (one) tma_stores_read();
+        tc::named_sync(1 + (warp - 4) / 4, 128);
+      };
+      auto send_stage = [&](int64_t tok0) {
+        tc::fence_async_smem();
+        tc::named_sync(1 + (warp - 4) / 4, 128);
+        if (one && ch0 < p.N && tok0 < p.M) tma_store(&ymap, at, (int)ch0, (int)tok0);
+      };
+      if (p.tma_out) free_stage();
       int v[2][32];
       tmem_get(src, v[0]);
 #pragma unroll
@@ -573,33 +593,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
           __syncwarp();
           if (lane == 0) arrive_remote(mapa(tc::smem_u32(acc_empty + b), 0));
         }
-        if (t0 + 32 * q >= p.M) continue;  // (the same in the four warps of a half)
-        if (!p.tma_out) {
-          store_any(p, c, t0 + 32 * q, xs[q], v[q & 1]);
-          continue;
-        }
-        const bool wide = p.dtype == SSMQ_F32;
-        uint8_t* buf = out + (warp - 4) / 4 * kHalfStage + (wide ? 0 : (q & 1) * (kHalfStage / 2));
-        const bool one = quarter == 0 && lane == 0;  // issues the half's stores
-        if (one) {
-          if (wide)
-            tma_stores_read<0>();
-          else
-            tma_stores_read<1>();
-        }
-        tc::named_sync(1 + (warp - 4) / 4, 128);
         const int col = quarter * 32 + lane;
-        if (wide)
-          stage_tokens<float>(c, xs[q], v[q & 1], buf + col * 4);
-        else if (p.dtype == SSMQ_F16)
-          stage_tokens<__half>(c, xs[q], v[q & 1], buf + col * 2);
-        else
-          stage_tokens<__nv_bfloat16>(c, xs[q], v[q & 1], buf + col * 2);
-        tc::fence_async_smem();
-        tc::named_sync(1 + (warp - 4) / 4, 128);
-        const int64_t ch0 = ch * kPairCh + rank * kRows;
-        if (one && ch0 < p.N) tma_store(&ymap, tc::smem_u32(buf), (int)ch0, (int)(t0 + 32 * q));
+        if (!p.tma_out) {
+          if (t0 + 32 * q < p.M) store_any(p, c, t0 + 32 * q, xs[q], v[q & 1]);
+        } else if (p.dtype == SSMQ_F32) {
+          if (q == 2) {
+            send_stage(t0);
+            free_stage();
+          }
+          stage_tokens<float>(c, xs[q], v[q & 1], at + ((q & 1) * 32 * kRows + col) * 4);
+        } else if (p.dtype == SSMQ_F16) {
+          stage_tokens<__half>(c, xs[q], v[q & 1], at + (q * 32 * kRows + col) * 2);
+        } else {
+          stage_tokens<__nv_bfloat16>(c, xs[q], v[q & 1], at + (q * 32 * kRows + col) * 2);
+        }
       }
+      if (p.tma_out) send_stage(p.dtype == SSMQ_F32 ? t0 + 64 : t0);
     }
     if (quarter == 0 && lane == 0)  // the stores are done before the CTA leaves
       asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -797,7 +806,7 @@ cudaError_t launch_int8_linear(const ssmq_linear_args& a, void* ws, cudaStream_t
   if (rows16(p.y, p.ldy, esz) && p.ldy < ((int64_t)1 << 36)) {
     const cuuint64_t dims[2] = {(cuuint64_t)p.N, (cuuint64_t)p.M};
     const cuuint64_t strides[1] = {(cuuint64_t)p.ldy * esz};
-    const cuuint32_t box[2] = {(cuuint32_t)kRows, 32};
+    const cuuint32_t box[2] = {(cuuint32_t)kRows, esz == 4 ? 64u : 128u};
     p.tma_out = encode_tiled(&ymap,
                              esz == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32
                                       : CU_TENSOR_MAP_DATA_TYPE_UINT16,
