@@ -35,10 +35,12 @@ struct NormParams {
   float* scales;
   int64_t xs, rs, ros, ys, cs;  // row strides in elements
   uint32_t* status;
+  bool w16;  // w on a 16-byte boundary
 };
 
-// codes of eight values at a scale whose reciprocal is usable; false when one
-// of them is not finite
+// Codes of eight values at a scale whose reciprocal is usable; false when one of
+// them is not finite.  No clamp: |v| <= max |v| and the scale is fl(max |v| / 127),
+// so the quotient is at most 127 (1 + 2^-22) and rounds to 127.
 __device__ __forceinline__ bool quant8(const float (&v)[8], float s, float rs, uint2& out) {
   const float2 r2 = make_float2(rs, rs), n2 = make_float2(-s, -s);
   const float2 mg = make_float2(12582912.0f, 12582912.0f), zero = make_float2(0.0f, 0.0f);
@@ -48,8 +50,6 @@ __device__ __forceinline__ bool quant8(const float (&v)[8], float s, float rs, u
   for (int i = 0; i < 8; i += 2) {
     float2 q = div2_rn(make_float2(v[i], v[i + 1]), n2, r2);
     nf = ffma2(q, zero, nf);
-    q.x = fminf(fmaxf(q.x, -127.0f), 127.0f);
-    q.y = fminf(fmaxf(q.y, -127.0f), 127.0f);
     const float2 m = fadd2(q, mg);
     mb[i] = __float_as_uint(m.x);
     mb[i + 1] = __float_as_uint(m.y);
@@ -64,9 +64,34 @@ enum {
   kAligned = 0,  // eight consecutive columns, rows on 16-byte boundaries
   kShifted = 1,  // eight consecutive columns on a 16-byte boundary of memory: the
                  // row starts `mis` elements into a piece (the same for every
-                 // tensor of 16- or 32-bit elements), its ends go by element
+                 // tensor of 16- or 32-bit elements).  What a piece at an end of
+                 // the row writes, and every piece's codes (whose rows start on a
+                 // boundary), go through shared memory
   kScalar = 2    // element e is column e * lanes + lane
 };
+
+// w[c8 - mis .. c8 - mis + 7] (c8 a multiple of 8, mis < 8) from the four aligned
+// 16-byte pieces around them, by three stages of selects: eight loads of single
+// weights, 32 bytes apart between lanes, cost four times the cache wavefronts.
+// Indices outside the row read some weight of it.
+__device__ __forceinline__ void shifted_weights(const float* w, int c8, int mis, int dim,
+                                                float (&o)[8]) {
+  const float4* w4 = reinterpret_cast<const float4*>(w);
+  const int last = (dim - 1) / 4;
+  float r[16];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float4 q = __ldg(w4 + max(0, min(c8 / 4 - 2 + k, last)));
+    r[4 * k] = q.x, r[4 * k + 1] = q.y, r[4 * k + 2] = q.z, r[4 * k + 3] = q.w;
+  }
+  float a[12], b[9];  // o[j] = r[j + 8 - mis]
+#pragma unroll
+  for (int i = 0; i < 12; ++i) a[i] = mis & 4 ? r[i] : r[i + 4];
+#pragma unroll
+  for (int i = 0; i < 9; ++i) b[i] = mis & 2 ? a[i + 1] : a[i + 3];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = mis & 1 ? b[j] : b[j + 1];
+}
 
 // kTpr lanes per row (at most a warp), or a CTA size bound: the whole CTA
 // holds one row.
@@ -76,6 +101,10 @@ __global__ void __launch_bounds__(kTpr <= 32 ? kSmallThreads : kTpr)
   __shared__ float s_sum[kMaxThreads / 32], s_max[kMaxThreads / 32];
   constexpr bool kInWarp = kTpr <= 32;
   constexpr bool kPieces = kMode != kScalar;
+  constexpr int kRowsCta = kInWarp ? kSmallThreads / (kInWarp ? kTpr : 1) : 1;
+  // kShifted: the two end pieces of a row, for residual_out and for y; the codes
+  __shared__ __align__(16) T s_ends[kMode == kShifted ? 2 : 1][kMode == kShifted ? kRowsCta : 1][16];
+  extern __shared__ __align__(16) uint64_t s_codes[];
   const int lanes = kInWarp ? kTpr : (int)blockDim.x;
   const int lane = kInWarp ? (int)threadIdx.x % kTpr : (int)threadIdx.x;
   const int64_t t0 = kInWarp ? (int64_t)blockIdx.x * (kSmallThreads / kTpr) + threadIdx.x / kTpr
@@ -102,25 +131,51 @@ __global__ void __launch_bounds__(kTpr <= 32 ? kSmallThreads : kTpr)
       if (whole(c)) {
         const Raw8<T> r = load8(q + c);
         unpack8<T>(r, o);
+      } else if (kMode == kShifted && c > -8 && c < p.dim) {
+        // an end of the row: the aligned 16 bytes around it, whose other elements
+        // (the next row's, or padding) are dropped; 16 bytes without an element of
+        // the row are not read
+        if constexpr (sizeof(T) == 2) {
+          const Raw8<T> r = load8(q + c);
+          unpack8<T>(r, o);
+        } else {
+          const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          const float4* g = reinterpret_cast<const float4*>(q + c);
+          unpack8<T>(Raw8<T>{c > -4 ? g[0] : zero, c + 4 < p.dim ? g[1] : zero}, o);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = inside(c + j) ? o[j] : 0.0f;
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          o[j] = kMode == kShifted && inside(c + j) ? to_f32(q[c + j]) : 0.0f;
+        for (int j = 0; j < 8; ++j) o[j] = 0.0f;
       }
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = to_f32(q[min(col(i, j), p.dim - 1)]);
     }
   };
-  auto write = [&](T* q, int i, const float (&v)[8]) {
+  auto meet = [&] {  // the row's threads
+    if constexpr (kInWarp)
+      __syncwarp();
+    else
+      __syncthreads();
+  };
+  const int row_cta = kInWarp ? (int)threadIdx.x / (kInWarp ? kTpr : 1) : 0;
+  // kShifted: the row's end pieces from shared memory, an element per lane
+  auto write_ends = [&](T* q, int which) {
+    const int tail = (p.dim + mis - 1) / 8 * 8 - mis;  // first column of the last piece
+    for (int e = lane; e < 16; e += lanes) {
+      const int c0 = e < 8 ? -mis : tail, c = c0 + e % 8;
+      if (inside(c) && !whole(c0) && (e < 8 || tail > -mis)) q[c] = s_ends[which][row_cta][e];
+    }
+  };
+  auto write = [&](T* q, int i, const float (&v)[8], int which) {
     const int c = col(i, 0);
     if constexpr (kPieces) {
       if (whole(c)) {
         store8(q + c, pack8<T>(v));
-      } else if (kMode == kShifted) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (inside(c + j)) q[c + j] = from_f32<T>(v[j]);
+      } else if (kMode == kShifted && c > -8 && c < p.dim) {
+        store8(&s_ends[kMode == kShifted ? which : 0][row_cta][c <= 0 ? 0 : 8], pack8<T>(v));
       }
     } else {
 #pragma unroll
@@ -150,51 +205,80 @@ __global__ void __launch_bounds__(kTpr <= 32 ? kSmallThreads : kTpr)
   }
   if (p.res_out && row) {
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) write(ro, i, v[i]);
+    for (int i = 0; i < kItems; ++i) write(ro, i, v[i], 0);
   }
 
+  // Sum of squares and the largest |r w|.  Columns outside the row hold 0, and a
+  // NaN is passed over by the maximum; an infinity is found afterwards.
 #pragma unroll
   for (int i = 0; i < kItems; ++i) {
     float w[8];
     const int c = col(i, 0);
     if (p.w) {
-      if constexpr (kMode == kAligned) {
-        if (c < p.dim) {
-          const Raw8<float> r = load8(p.w + c);
-          unpack8<float>(r, w);
+      if (kMode == kAligned && whole(c)) {
+        const Raw8<float> r = load8(p.w + c);
+        unpack8<float>(r, w);
+      } else if (kMode == kShifted && p.w16 && c > -8 && c < p.dim) {
+        shifted_weights(p.w, c + mis, mis, p.dim, w);
+        if (!whole(c)) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) w[j] = inside(c + j) ? w[j] : 0.0f;
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = __ldg(p.w + max(0, min(col(i, j), p.dim - 1)));
+        for (int j = 0; j < 8; ++j)
+          w[j] = kMode != kAligned && inside(col(i, j)) ? __ldg(p.w + col(i, j)) : 0.0f;
       }
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const bool in = inside(col(i, j));
-      if (kMode == kScalar && !in) v[i][j] = 0.0f;
+      if (kMode == kScalar && !inside(col(i, j))) v[i][j] = 0.0f;
       sum = fmaf(v[i][j], v[i][j], sum);
-      if (p.w) v[i][j] = in ? v[i][j] * w[j] : 0.0f;
-      const float m = fabsf(v[i][j]);
-      mx = isfinite(m) ? fmaxf(mx, m) : mx;
+      if (p.w) v[i][j] *= w[j];
+      mx = fmaxf(mx, fabsf(v[i][j]));
     }
   }
+  auto reduce = [&](float& add, float& most) {
 #pragma unroll
-  for (int o = (kInWarp ? kTpr : 32) / 2; o > 0; o >>= 1) {
-    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-  }
-  if constexpr (!kInWarp) {
-    const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    if ((threadIdx.x & 31) == 0) s_sum[warp] = sum, s_max[warp] = mx;
-    __syncthreads();
-    const int l = threadIdx.x & 31;
-    sum = l < nw ? s_sum[l] : 0.0f;
-    mx = l < nw ? s_max[l] : 0.0f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-      mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+    for (int o = (kInWarp ? kTpr : 32) / 2; o > 0; o >>= 1) {
+      add += __shfl_xor_sync(0xFFFFFFFFu, add, o);
+      most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
     }
+    if constexpr (!kInWarp) {
+      const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+      if ((threadIdx.x & 31) == 0) s_sum[warp] = add, s_max[warp] = most;
+      __syncthreads();
+      const int l = threadIdx.x & 31;
+      add = l < nw ? s_sum[l] : 0.0f;
+      most = l < nw ? s_max[l] : 0.0f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        add += __shfl_xor_sync(0xFFFFFFFFu, add, o);
+        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+      }
+    }
+  };
+  reduce(sum, mx);
+  if constexpr (kMode == kShifted) {
+    if (p.res_out) {
+      if constexpr (kInWarp) __syncwarp();  // (a CTA's row has met in the reduction)
+      if (row) write_ends(ro, 0);
+    }
+  }
+  // an infinite product (in any row of this warp, or in the CTA's row): the maximum
+  // over the finite ones
+  if (__any_sync(0xFFFFFFFFu, mx > 3.40282347e+38f)) {
+    mx = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float m = fabsf(v[i][j]);
+        mx = isfinite(m) ? fmaxf(mx, m) : mx;
+      }
+    if constexpr (!kInWarp) __syncthreads();  // (s_max is read)
+    float none = 0.0f;
+    reduce(none, mx);
   }
 
   uint32_t flags = 0;
@@ -204,7 +288,7 @@ __global__ void __launch_bounds__(kTpr <= 32 ? kSmallThreads : kTpr)
   // (eps = 0 and a zero row: 0 * inf; an overflowing maximum has no finite scale)
   const float s = good && isfinite(amax) ? __fdiv_rn(amax, 127.0f) : 0.0f;
   const float rs = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
-  const bool fast = usable_recip(s, rs);
+  const bool fast = s > 0.0f && usable_recip(s, rs);
   if (!good) flags |= SSMQ_DEV_NONFINITE;
   if (p.scales && lane == 0 && row) p.scales[t] = s;
 
@@ -215,10 +299,10 @@ __global__ void __launch_bounds__(kTpr <= 32 ? kSmallThreads : kTpr)
     const int c = col(i, 0);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[i][j] *= rstd;
-    if (p.y && row) write(y, i, v[i]);
+    if (p.y && row) write(y, i, v[i], kMode == kShifted ? 1 : 0);
     if (!p.codes) continue;
     uint2 out = make_uint2(0u, 0u);
-    if (!(s > 0.0f && fast && quant8(v[i], s, rs, out))) {
+    if (!(fast && quant8(v[i], s, rs, out))) {
       uint32_t b[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -231,39 +315,31 @@ __global__ void __launch_bounds__(kTpr <= 32 ? kSmallThreads : kTpr)
     if constexpr (kMode == kAligned) {
       if (c < p.dim && row) *reinterpret_cast<uint2*>(q + c) = out;
     } else if constexpr (kMode == kShifted) {
-      // The piece's codes start `mis` bytes before an 8-byte boundary of the
-      // codes' row: the word behind that boundary takes the rest of this piece
-      // and the head of the next lane's.  At the ends of a warp (or of the
-      // row's lanes), where no lane to the right is at hand, codes go by byte.
-      constexpr int kGroup = kInWarp ? kTpr : 32;
-      const int g = lane % kGroup;
-      const uint64_t own = (uint64_t)out.x | ((uint64_t)out.y << 32);
-      const uint64_t right = __shfl_down_sync(0xFFFFFFFFu, own, 1, kGroup);
-      const bool edge = mis > 0 && g == kGroup - 1;
-      if (row) {
-        const int at = c + mis;
-        if (!edge && at + 8 <= p.dim) {
-          const uint64_t word = mis ? (own >> (8 * mis)) | (right << (64 - 8 * mis)) : own;
-          *reinterpret_cast<uint64_t*>(q + at) = word;
-        } else {
-          const int n = edge ? 8 - mis : 8;
-          const uint64_t word =
-              mis && !edge ? (own >> (8 * mis)) | (right << (64 - 8 * mis)) : own >> (8 * mis);
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < n && at + j < p.dim) q[at + j] = (int8_t)(word >> (8 * j));
-        }
-        if (g == 0 && mis > 0) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < mis && inside(c + j)) q[c + j] = (int8_t)(own >> (8 * j));
-        }
-      }
+      s_codes[(kInWarp ? row_cta * kItems * kTpr : 0) + i * lanes + lane] =
+          (uint64_t)out.x | ((uint64_t)out.y << 32);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (row && inside(col(i, j)))
           q[col(i, j)] = (int8_t)((j < 4 ? out.x : out.y) >> (8 * (j & 3)));
+    }
+  }
+  if constexpr (kMode == kShifted) {
+    meet();
+    if (p.y && row) write_ends(y, 1);
+    if (p.codes && row) {
+      // aligned words of codes: bytes mis .. of a piece, then the next piece's head
+      const uint64_t* from = s_codes + (kInWarp ? row_cta * kItems * kTpr : 0);
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) {
+        const int k = i * lanes + lane;
+        if (k * 8 + 8 > p.dim) continue;
+        uint64_t word = from[k];
+        if (mis) word = (word >> (8 * mis)) | (from[k + 1] << (64 - 8 * mis));
+        *reinterpret_cast<uint64_t*>(q + k * 8) = word;
+      }
+      const int8_t* bytes = reinterpret_cast<const int8_t*>(from);
+      for (int c = p.dim / 8 * 8 + lane; c < p.dim; c += lanes) q[c] = bytes[c + mis];
     }
   }
   if (row) flag_status(p.status, flags);
@@ -274,10 +350,12 @@ cudaError_t launch_row(const NormParams& p, int lanes, cudaStream_t st) {
   if (kTpr <= 32) {
     const int rows = kSmallThreads / (kTpr <= 32 ? kTpr : 32);
     rms_norm_quantize_kernel<T, kItems, kTpr, kMode>
-        <<<(unsigned)((p.tokens + rows - 1) / rows), kSmallThreads, 0, st>>>(p);
+        <<<(unsigned)((p.tokens + rows - 1) / rows), kSmallThreads,
+           kMode == kShifted ? kSmallThreads * kItems * 8 : 0, st>>>(p);
   } else {
     rms_norm_quantize_kernel<T, kItems, kTpr, kMode>
-        <<<(unsigned)p.tokens, (unsigned)((lanes + 31) / 32 * 32), 0, st>>>(p);
+        <<<(unsigned)p.tokens, (unsigned)((lanes + 31) / 32 * 32),
+           kMode == kShifted ? (size_t)((lanes + 31) / 32 * 32) * kItems * 8 : 0, st>>>(p);
   }
   return cudaGetLastError();
 }
@@ -342,6 +420,7 @@ cudaError_t launch_rms_norm_quantize(const ssmq_norm_args& a, cudaStream_t st) {
   p.ys = a.y_stride;
   p.cs = a.codes_stride;
   p.status = a.status;
+  p.w16 = (reinterpret_cast<uintptr_t>(a.weight) & 15u) == 0;
   switch (a.dtype) {
     case SSMQ_F16: return launch_type<__half>(p, st);
     case SSMQ_BF16: return launch_type<__nv_bfloat16>(p, st);

@@ -198,3 +198,21 @@ def test_other_stream_and_graph():
     torch.cuda.synchronize()
     for t, u, v in zip(ref, a, (codes, scales, r)):
         assert torch.equal(t, u) and torch.equal(t, v)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("d", list(range(1, 26)) + [63, 65, 127, 129, 255, 257, 511, 515, 1001])
+def test_rows_off_16_byte_boundaries(dtype, d):
+    """Every distance of a row's start from a 16-byte boundary: rows of d
+    elements in a buffer, the first of them shifted as well."""
+    T = 9
+    for shift in (0, 1, 3):
+        buf = make(d, (3, T * d + 16), dtype).to(dev())
+        x, res = (buf[k, shift:shift + T * d].view(T, d) for k in (0, 1))
+        out = torch.full((2, T * d + 16), 7.0, dtype=dtype, device=dev())
+        r, y = (out[k, shift:shift + T * d].view(T, d) for k in (0, 1))
+        w = make(d + 1, (d,), F32)
+        codes, scales, r, y = api.rms_norm_quantize(x, w.to(dev()), residual=res, residual_out=r, y=y)
+        check(x.cpu(), w, res.cpu(), 1e-5, codes, scales, r, y)
+        rest = torch.cat((out[:, :shift], out[:, shift + T * d:]), 1)
+        assert (rest == 7).all()
