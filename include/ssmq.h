@@ -793,8 +793,8 @@ ssmq_status ssmq_int8_linear(const ssmq_linear_args* args, void* workspace, size
  *
  * Layouts (b = batch, L = seqlen, d = dim): v, g, z, y, dy, dv, dg, dz are
  * (b, L, d) of dtype, element (i, t, c) at i * batch_stride + t * row_stride + c
- * (row_stride >= d unless L is 1; batch_stride >= 0, for an output large
- * enough that sequences do not overlap).  h0, h_final, dh0, dh_final: fp32
+ * (row_stride >= d unless L is 1; batch_stride >= 0, for an output such that
+ * its sequences do not overlap: one behind the other, or row by row).  h0, h_final, dh0, dh_final: fp32
  * (b, d), dense; NULL h0 / dh_final: zeros.  h_final may be h0 and dh0 may be
  * dh_final (the same address).
  * lengths: device int32[b] or NULL.  Sequence i has lengths[i] steps (values
@@ -819,9 +819,10 @@ ssmq_status ssmq_int8_linear(const ssmq_linear_args* args, void* workspace, size
  *
  * status: device word or NULL, SSMQ_DEV_TIMEOUT if a bounded device wait gave up.
  * The order of every sum depends on the sizes alone: a call repeated on the
- * same inputs gives the same bytes.  No workspace; any L >= 0, any d.
+ * same inputs on the same alignments gives the same bytes.  No workspace.
  * Errors: INVALID_ARG (NULL, negative sizes, bad strides, overlaps),
- * ALIGNMENT (base not on an element), UNSUPPORTED (b * ceil(d / 16) > 2^27).
+ * ALIGNMENT (base not on an element), UNSUPPORTED (b * ceil(d / 16) > 2^27,
+ * L >= 2^31).
  */
 typedef struct {
   void* p;                  /* device, NULL where the tensor is absent */

@@ -637,8 +637,10 @@ ssmq_status check_rows(const void* p, int64_t b, int64_t L, int64_t d, int64_t b
   const __int128 rows = (L > 1 ? (__int128)(L - 1) * rs : 0) + d;
   const __int128 all = (b > 1 ? (__int128)(b - 1) * bs : 0) + rows;
   REQUIRE(all < ((__int128)1 << 59), SSMQ_ERR_INVALID_ARG, "%s: %s: size overflow", fn, name);
-  REQUIRE(!out || b == 1 || bs >= rows, SSMQ_ERR_INVALID_ARG,
-          "%s: %s: batch stride %lld makes sequences overlap", fn, name, (long long)bs);
+  // sequence after sequence, or row after row with the sequences interleaved
+  REQUIRE(!out || b == 1 || bs >= rows || (bs >= d && (__int128)(b - 1) * bs + d <= rs),
+          SSMQ_ERR_INVALID_ARG, "%s: %s: batch stride %lld makes sequences overlap", fn, name,
+          (long long)bs);
   r->lo = reinterpret_cast<uintptr_t>(p);
   r->hi = r->lo + (uintptr_t)all * e;
   r->bs = b > 1 ? bs * e : 0;
@@ -662,11 +664,15 @@ bool same(const Region& a, const Region& b) {
 // slices of one tensor (equal strides, disjoint columns) do not.
 bool overlap(const Region& a, const Region& b) {
   if (!a.any() || !b.any() || a.hi <= b.lo || b.hi <= a.lo) return false;
-  if (a.rs > 0 && a.rs == b.rs && a.bs == b.bs && a.bs % a.rs == 0) {
-    const int64_t off = (int64_t)((a.lo < b.lo ? b.lo - a.lo : a.lo - b.lo) % (uintptr_t)a.rs);
-    const int64_t first = a.lo < b.lo ? a.width : b.width;
-    const int64_t second = a.lo < b.lo ? b.width : a.width;
-    if (off >= first && off + second <= a.rs) return false;
+  if (a.rs == b.rs && a.bs == b.bs) {
+    // every row of both starts a multiple of `unit` behind the first
+    const int64_t less = a.rs < a.bs ? a.rs : a.bs, more = a.rs < a.bs ? a.bs : a.rs;
+    const int64_t unit = less > 0 ? (more % less == 0 ? less : 0) : more;
+    if (unit > 0) {
+      const bool ab = a.lo < b.lo;
+      const int64_t off = (int64_t)((ab ? b.lo - a.lo : a.lo - b.lo) % (uintptr_t)unit);
+      if (off >= (ab ? a.width : b.width) && off + (ab ? b.width : a.width) <= unit) return false;
+    }
   }
   return true;
 }
@@ -694,9 +700,9 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 ssmq_status check_gated_sizes(int64_t b, int64_t L, int64_t d, int32_t dtype, const char* fn) {
   REQUIRE(is_dtype(dtype), SSMQ_ERR_INVALID_ARG, "%s: bad dtype %d", fn, (int)dtype);
   REQUIRE(b >= 0 && L >= 0 && d >= 0, SSMQ_ERR_INVALID_ARG, "%s: negative size", fn);
-  REQUIRE(b < ((int64_t)1 << 31) && d < ((int64_t)1 << 31) && L < ((int64_t)1 << 40) &&
+  REQUIRE(b < ((int64_t)1 << 31) && d < ((int64_t)1 << 31) && L < ((int64_t)1 << 31) &&
               b * ((d + 15) / 16) <= ((int64_t)1 << 27),
-          SSMQ_ERR_UNSUPPORTED, "%s: too many channels", fn);
+          SSMQ_ERR_UNSUPPORTED, "%s: too many steps or channels", fn);
   return SSMQ_OK;
 }
 

@@ -349,14 +349,17 @@ __device__ __forceinline__ float2 carry_in(Shared<TileT>& sh, int64_t k, float4 
       flags |= SSMQ_DEV_TIMEOUT;
     __syncwarp();
     float2 s = h;
-    // (two at a time, a power of two in all: the loads do not wait on one another)
-#pragma unroll 2
-    for (uint32_t r = 0; r < size; r += 2) {
-      const float4 m0 = sh.cta[buf][r][l], m1 = sh.cta[buf][r + 1][l];
-      if (r == rank) base = s;
-      s = apply(m0, s);
-      if (r + 1 == rank) base = s;
-      s = apply(m1, s);
+    // (four loads at a time, which do not wait on one another; size is 2, 4, 8 or 16,
+    // and the entries of a cluster of 2 end after two)
+    for (uint32_t r = 0; r < size; r += 4) {
+      float4 e[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e[i] = sh.cta[buf][r + i][l];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (r + i == rank) base = s;
+        if (i < 2 || size > 2) s = apply(e[i], s);
+      }
     }
     h = s;
   } else {
@@ -395,7 +398,7 @@ inline Shape shape_for(int64_t b, int64_t L, int64_t d, int64_t resident, int fi
   };
   s.narrow = false;
   int64_t n = pick(kWideChannels, kWideLen, 8);
-  if (n < resident) {
+  if (n < resident * 85 / 100) {
     const Shape wide = s;
     s.narrow = true;
     const int64_t m = pick(kNarrowChannels, kNarrowLen, kMaxCluster);

@@ -360,6 +360,54 @@ def test_repeatable_streams_and_graph():
         assert torch.equal(a, b) and torch.equal(a, c) and torch.equal(a, e)
 
 
+@pytest.mark.parametrize("d", [64, 50, 33])
+def test_layouts(d):
+    """Time-major tensors, inputs shared by the batch (batch stride 0) and
+    single-row tensors with odd strides give the contiguous call's values."""
+    p = problem(22, 3, 200, d, F16, strided=False)
+    ref = Ref(p["v"], p["g"], p["z"], p["h0"], None, p["dy"], p["dh"])
+    tm = {k: p[k].transpose(0, 1).contiguous().transpose(0, 1) for k in ("v", "g", "z", "dy")}
+    y = torch.empty_like(tm["v"])
+    y, h, st = api.gated_scan(tm["v"], tm["g"], z=tm["z"], h0=p["h0"], y=y, save_states=True)
+    ref.close("y", y)
+    for name, t in zip(("dv", "dg", "dz", "dh0"), api.gated_scan_backward(
+            tm["dy"], tm["v"], tm["g"], st, z=tm["z"], dh_final=p["dh"])):
+        ref.close(name, t)
+    shared = {k: p[k][:1].expand(3, -1, -1) for k in ("v", "g", "z")}
+    ref = Ref(shared["v"], shared["g"], shared["z"], p["h0"], None, p["dy"], p["dh"])
+    y, h, st = api.gated_scan(shared["v"], shared["g"], z=shared["z"], h0=p["h0"],
+                              save_states=True)
+    ref.close("y", y)
+    for name, t in zip(("dv", "dg", "dz", "dh0"), api.gated_scan_backward(
+            p["dy"], shared["v"], shared["g"], st, z=shared["z"], dh_final=p["dh"])):
+        ref.close(name, t)
+    one = {k: torch.as_strided(p[k], (1, 1, d), (7, 1, 1)) for k in ("v", "g")}
+    y, _ = api.gated_scan(one["v"], one["g"])
+    Ref(one["v"], one["g"]).close("y", y)
+
+
+def test_broadcast_leaves_sum_their_gradients():
+    """A leaf shared by the batch gets the sum of the sequences' gradients."""
+    p = problem(23, 4, 90, 24, F32, strided=False)
+    v, g = p["v"][:1].clone().requires_grad_(), p["g"][:1].clone().requires_grad_()
+    z = p["z"].clone().requires_grad_()
+    y, h = api.gated_scan(v.expand(4, -1, -1), g.expand(4, -1, -1), z=z)
+    got = torch.autograd.grad(y, (v, g, z), p["dy"])
+    ev, eg = p["v"][:1].expand(4, -1, -1), p["g"][:1].expand(4, -1, -1)
+    _, _, st = api.gated_scan(ev, eg, z=p["z"], save_states=True)
+    ref = api.gated_scan_backward(p["dy"], ev, eg, st, z=p["z"])
+    assert torch.equal(got[0], ref[0].sum(0, keepdim=True))
+    assert torch.equal(got[1], ref[1].sum(0, keepdim=True)) and torch.equal(got[2], ref[2])
+
+
+def test_status_stays_clear():
+    st = torch.zeros(1, dtype=torch.int32, device=dev())
+    p = problem(24, 2, 700, 64, F16)
+    _, _, states = api.gated_scan(p["v"], p["g"], z=p["z"], save_states=True, status=st)
+    api.gated_scan_backward(p["dy"], p["v"], p["g"], states, z=p["z"], status=st)
+    assert int(st) == 0
+
+
 def test_first_call_of_a_thread():
     """A thread that has made no CUDA call yet gets the same bytes: the same
     kernels run (tensor maps need the thread's context)."""

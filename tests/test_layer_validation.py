@@ -128,6 +128,7 @@ def test_gated_scan(L):
     assert S(dtype=7) == N.ERR_INVALID_ARG
     assert S(seqlen=-1) == N.ERR_INVALID_ARG
     assert S(batch=1 << 30, dim=1 << 20) == N.ERR_UNSUPPORTED
+    assert S(seqlen=1 << 31) == N.ERR_UNSUPPORTED
     assert S(v=None) == N.ERR_INVALID_ARG
     assert S(y=None) == N.ERR_INVALID_ARG
     assert S(g=A + 1) == N.ERR_ALIGNMENT
@@ -158,6 +159,15 @@ def test_gated_scan_fault_injection(L, monkeypatch):
         cols.update({n: A + 64 * i, n + "_batch_stride": 12800, n + "_row_stride": 128})
     assert S(**cols) == N.ERR_CUDA
     cols["y"] = A + 64 * 3 - 2
+    assert S(**cols) == N.ERR_INVALID_ARG
+    for i, n in enumerate(("v", "g", "z", "y")):  # the same, rows of both sequences in turn
+        cols.update({n: A + 64 * i, n + "_batch_stride": 128, n + "_row_stride": 256})
+    assert S(**cols) == N.ERR_CUDA
+    cols["y"] = A + 64 * 3 + 2
+    assert S(**cols) == N.ERR_INVALID_ARG
+    for n in ("v", "g", "z", "y"):  # interleaved unevenly: not told apart
+        cols.update({n + "_batch_stride": 128, n + "_row_stride": 300})
+    cols["y"] = A + 64 * 3
     assert S(**cols) == N.ERR_INVALID_ARG
 
 
