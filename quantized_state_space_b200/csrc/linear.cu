@@ -248,7 +248,7 @@ __device__ __forceinline__ void tma_stores_read() {
 // parts (32-bit integers pushed through distributed shared memory: exact, no
 // workspace, no second launch).
 constexpr int kSplitThreads = 192;  // 4 epilogue warps, 1 TMA, 1 MMA
-constexpr int kMaxSplit = 8;
+constexpr int kMaxSplit = 4;  // (clusters of 8 such CTAs waited for SMs: 12 us against 8)
 
 template <int kTok>
 struct SplitCfg {
@@ -689,19 +689,48 @@ cudaError_t encode(CUtensorMap* map, const void* p, int64_t rows, int64_t k, int
                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
+// Which kernel, tile and split: the smallest estimate of the time beyond the
+// start that all share.  Measured on one B200 (us, device): a CTA takes in its
+// operands at about 92 KB/us; exchanging parts of K costs 1.7 + 0.035 per token
+// column; a round of the pair kernel costs 0.36 per 128 bytes of K, plus 1.6.
+// Tokens x channels x K, the tile taken against the next best: 512 x 4096 x 4096
+// 128 columns 14.0, pairs 16.0; 1024 x 4096 x 4096 pairs 17.0, 128 columns 19.0;
+// 256 x 4096 x 1024 64 columns 6.5, 128 columns and 2 parts 12.7; 64 x 4096 x 8192
+// 64 columns and 4 parts 13.6, 32 and 2 parts 15.5; 200 x 1000 x 1024 16 columns
+// 5.6, 32 columns and 2 parts 7.4.
+struct Plan {
+  bool pair;
+  int tok, split;
+};
+Plan plan_for(int64_t M, int64_t N, int kblocks, int sms) {
+  Plan best = {false, 16, 1};
+  double least = 1e300;
+  const int64_t ch = (N + kRows - 1) / kRows;
+  for (int tok = 16; tok <= 128; tok *= 2) {
+    if (tok > 16 && tok >= 2 * M) break;  // (half the columns would be idle)
+    const int64_t tiles = ch * ((M + tok - 1) / tok);
+    for (int split = 1; split <= kMaxSplit && kblocks >= 4 * split; split *= 2) {
+      if (split > 1 && tiles * split > sms) break;
+      const double bytes = (double)((kblocks + split - 1) / split) * (kRows + tok) * kBlockK;
+      const double fill = (double)(tiles * split) / sms;
+      const double us = bytes / 92e3 * (fill > 1 ? fill : 1) + (split > 1 ? 1.7 + 0.035 * tok : 0);
+      if (us < least) least = us, best = {false, tok, split};
+    }
+  }
+  const int64_t pairs = ((M + kPairTok - 1) / kPairTok) * ((N + kPairCh - 1) / kPairCh);
+  const int64_t rounds = (pairs + sms / 2 - 1) / (sms / 2);
+  if (M > 128 && 1.6 + 0.36 * (double)rounds * kblocks < least) best.pair = true;
+  return best;
+}
+
 template <int kTok>
-cudaError_t launch_split(const CUtensorMap& wmap, const CUtensorMap& xmap, LinParams p,
+cudaError_t launch_split(const CUtensorMap& wmap, const CUtensorMap& xmap, LinParams p, int split,
                          cudaStream_t st) {
   using Cfg = SplitCfg<kTok>;
   p.ch_tiles = (p.N + kRows - 1) / kRows;
   p.tok_tiles = (p.M + kTok - 1) / kTok;
   const int64_t tiles = p.ch_tiles * p.tok_tiles;
   if (tiles > 0x7fffffff / kMaxSplit) return cudaErrorInvalidConfiguration;
-  int split = 1;
-  // parts of K while the CTAs fit the SMs once and a part keeps four K blocks
-  while (split < kMaxSplit && split < kTok / 4 && tiles * split * 2 <= sm_count() &&
-         p.kblocks >= 8 * split)
-    split *= 2;
   // One CTA per SM takes all the stages that fit (or that its K needs); several
   // share the shared memory two to an SM.
   const int room = (tiles * split <= sm_count() ? 224 : 110) * 1024;
@@ -777,22 +806,18 @@ cudaError_t launch_int8_linear(const ssmq_linear_args& a, void* ws, cudaStream_t
   if (!tma_rows(x, p.M, xst) && (e = align_rows(x, xst, p.M)) != cudaSuccess) return e;
   if (!tma_rows(w, p.N, wst) && (e = align_rows(w, wst, p.N)) != cudaSuccess) return e;
 
-  // Enough 256 x 256 tiles for every CTA pair: the pair kernel.  Fewer: smaller
-  // tiles, so that more SMs take part.
   const int sms = sm_count();
-  const int64_t pair_tiles = ((p.M + kPairTok - 1) / kPairTok) * ((p.N + kPairCh - 1) / kPairCh);
-  const bool pair = p.M > 128 && pair_tiles >= sms / 2;
-  int tok = pair ? kRows : 128;
-  if (!pair && p.M <= 64) tok = p.M <= 16 ? 16 : (p.M <= 32 ? 32 : 64);
+  const Plan plan = plan_for(p.M, p.N, p.kblocks, sms);
+  const int tok = plan.pair ? kRows : plan.tok;
   CUtensorMap wmap, xmap;
   if ((e = encode(&wmap, w, p.N, a.in_features, wst, kRows)) != cudaSuccess) return e;
   if ((e = encode(&xmap, x, p.M, a.in_features, xst, tok)) != cudaSuccess) return e;
-  if (!pair) {
+  if (!plan.pair) {
     switch (tok) {
-      case 16: return launch_split<16>(wmap, xmap, p, st);
-      case 32: return launch_split<32>(wmap, xmap, p, st);
-      case 64: return launch_split<64>(wmap, xmap, p, st);
-      default: return launch_split<128>(wmap, xmap, p, st);
+      case 16: return launch_split<16>(wmap, xmap, p, plan.split, st);
+      case 32: return launch_split<32>(wmap, xmap, p, plan.split, st);
+      case 64: return launch_split<64>(wmap, xmap, p, plan.split, st);
+      default: return launch_split<128>(wmap, xmap, p, plan.split, st);
     }
   }
   p.tok_tiles = (p.M + kPairTok - 1) / kPairTok;
@@ -813,6 +838,7 @@ cudaError_t launch_int8_linear(const ssmq_linear_args& a, void* ws, cudaStream_t
                              2, p.y, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE,
                              CU_TENSOR_MAP_L2_PROMOTION_NONE) == cudaSuccess;
   }
+  const int64_t pair_tiles = p.tok_tiles * p.ch_tiles;
   const int64_t pairs = pair_tiles < sms / 2 ? pair_tiles : sms / 2;
   int8_linear_pair_kernel<<<(unsigned)(2 * pairs), kPairThreads, kPairSmem, st>>>(wmap, xmap, ymap,
                                                                                   p);
