@@ -2,14 +2,14 @@
 // the tile of one CTA, its loads, and the exchange of carried states between
 // the CTAs of a cluster.
 //
-// A CTA owns a block of channels and, per round, one tile of consecutive
-// steps: kLanes lanes hold two channels each, every thread eight consecutive
-// steps of its channels in registers, so a warp holds 32 / kLanes segments
-// and the CTA kWarps * 32 / kLanes.  A segment acts on the state entering it
-// as h -> A h + B; (A, B) of segments, warps and CTAs compose in step order.
-// The CTAs of a cluster hold consecutive tiles and push their (A, B) into
-// each other's shared memory; one exchange per round replaces a pass over the
-// data or a spin on global memory.
+// A CTA owns a block of channels and, per round, one tile of consecutive steps:
+// kLanes lanes hold two channels each, every thread kSteps consecutive steps of
+// its channels, so a warp holds 32 / kLanes segments and the CTA kWarps times as
+// many.  A segment acts on the state entering it as h -> A h + B; (A, B) of
+// segments, warps and CTAs compose in step order.  The CTAs of a cluster hold
+// consecutive tiles and push their (A, B) into each other's shared memory; one
+// exchange per round replaces a second pass over the data or a spin on global
+// memory.
 #pragma once
 
 #include "internal.h"
@@ -301,10 +301,11 @@ __device__ __forceinline__ void carry_done(uint32_t size) {
 // State entering this thread's segment, from the segments' maps in step order
 // (kReverse: in reverse step order, the last segment of the warp, warp and
 // CTA first), and the state behind the whole round in h.  Every thread of the
-// cluster calls it, round by round.  Buffers alternate between rounds: a CTA pushes
-// round k + 2 only after it has every map of round k + 1, and a CTA pushes
-// round k + 1 only when its threads are done with round k.  met() runs behind the CTA's
-// barrier: every thread is done with the rounds before this one.
+// cluster calls it, round by round.  Buffers alternate between rounds: a CTA
+// pushes round k + 2 only after it has every map of round k + 1, and a CTA pushes
+// round k + 1 only when its threads are done with round k.  met() runs behind the
+// CTA's barrier: every thread is done with the rounds before this one, and with
+// what it read of this round before the call.
 template <typename TileT, bool kReverse, typename Met>
 __device__ __forceinline__ float2 carry_in(Shared<TileT>& sh, int64_t k, float4 m, float2& h,
                                            uint32_t rank, uint32_t size, uint32_t& flags,

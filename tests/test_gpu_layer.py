@@ -195,3 +195,31 @@ def test_training_step_through_the_projection():
     ref.close("dg", wide[..., d:2 * d])
     ref.close("dz", wide[..., 2 * d:])
     assert torch.equal(proj.grad, wide)
+
+
+def test_operators_side_by_side():
+    """Scans with clusters, gradients, CTA-pair and split products and norms on
+    four streams at once give what they give alone."""
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(3000, 1024, generator=g).half().to(dev())
+    q = torch.randint(-127, 128, (3000, 1024), generator=g, dtype=torch.int8).to(dev())
+    s = torch.rand(3000, generator=g).to(dev())
+    p = torch.randn(2, 1500, 3 * 64, generator=g).half().to(dev())
+    v, gg, z = p[..., :64], p[..., 64:128], p[..., 128:]
+    _, _, st = api.gated_scan(v, gg, z=z, save_states=True)
+    jobs = [lambda: api.rms_norm_quantize(x),
+            lambda: (api.int8_linear(q, s, q, s), api.int8_linear(q[:5], s[:5], q, s)),
+            lambda: api.gated_scan(v, gg, z=z),
+            lambda: api.gated_scan_backward(z, v, gg, st, z=z)]
+    refs = [job() for job in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    outs = [[] for _ in jobs]
+    for _ in range(8):
+        for job, stream, out in zip(jobs, streams, outs):
+            with torch.cuda.stream(stream):
+                out.append(job())
+    torch.cuda.synchronize()
+    for ref, out in zip(refs, outs):
+        for got in out:
+            assert all(torch.equal(a, b) for a, b in zip(ref, got))
