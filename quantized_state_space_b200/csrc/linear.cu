@@ -625,19 +625,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
 // Operands whose base or stride TMA cannot take are copied once to rows of a
 // multiple of 16 bytes (zero-padded): one aligned 16-byte store per thread,
 // its bytes gathered from aligned 32-bit words.
-__global__ void __launch_bounds__(256) align_rows_kernel(const int8_t* src, int64_t stride,
-                                                         int64_t rows, int64_t len, int8_t* dst,
-                                                         int64_t pitch) {
+struct AlignJob {
+  const int8_t* src;
+  int64_t stride, rows;
+  int8_t* dst;
+};
+__global__ void __launch_bounds__(256) align_rows_kernel(const AlignJob a, const AlignJob b,
+                                                         int64_t len, int64_t pitch) {
   const int64_t per = pitch / 16;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= rows * per) return;
+  int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const bool second = i >= a.rows * per;  // one launch for both operands
+  if (second) i -= a.rows * per;
+  if (i >= (second ? b.rows : a.rows) * per) return;
   const int64_t r = i / per, c = (i % per) * 16;
-  const int8_t* s = src + r * stride + c;
+  const int8_t* s = (second ? b.src : a.src) + r * (second ? b.stride : a.stride) + c;
+  int8_t* dst = second ? b.dst : a.dst;
   uint32_t w[4] = {0, 0, 0, 0};
   if (c + 16 <= len) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(s);
-    const int sh = (int)(a & 3) * 8;
-    const uint32_t* q = reinterpret_cast<const uint32_t*>(a & ~(uintptr_t)3);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(s);
+    const int sh = (int)(at & 3) * 8;
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(at & ~(uintptr_t)3);
     if (sh == 0) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) w[k] = q[k];
@@ -792,19 +799,22 @@ cudaError_t launch_int8_linear(const ssmq_linear_args& a, void* ws, cudaStream_t
   int64_t xst = a.x_stride, wst = a.w_stride;
   const int64_t pitch = pitch_of(a.in_features);
   uint8_t* room = static_cast<uint8_t*>(ws);
-  auto align_rows = [&](const int8_t*& t, int64_t& stride, int64_t rows) {
-    int8_t* dst = reinterpret_cast<int8_t*>(room);
-    const int64_t n = rows * (pitch / 16);
-    align_rows_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(t, stride, rows, a.in_features,
-                                                                   dst, pitch);
-    room += up256((size_t)rows * pitch);
-    t = dst;
-    stride = pitch;
-    return cudaGetLastError();
-  };
   cudaError_t e;
-  if (!tma_rows(x, p.M, xst) && (e = align_rows(x, xst, p.M)) != cudaSuccess) return e;
-  if (!tma_rows(w, p.N, wst) && (e = align_rows(w, wst, p.N)) != cudaSuccess) return e;
+  AlignJob jobs[2] = {};
+  auto job = [&](AlignJob& j, const int8_t*& t, int64_t& stride, int64_t rows) {
+    if (tma_rows(t, rows, stride)) return;
+    j = AlignJob{t, stride, rows, reinterpret_cast<int8_t*>(room)};
+    room += up256((size_t)rows * pitch);
+    t = j.dst;
+    stride = pitch;
+  };
+  job(jobs[0], x, xst, p.M);
+  job(jobs[1], w, wst, p.N);
+  if (const int64_t n = (jobs[0].rows + jobs[1].rows) * (pitch / 16)) {
+    align_rows_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(jobs[0], jobs[1], a.in_features,
+                                                                   pitch);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
 
   const int sms = sm_count();
   const Plan plan = plan_for(p.M, p.N, p.kblocks, sms);
