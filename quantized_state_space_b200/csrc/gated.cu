@@ -49,18 +49,24 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T
   const int64_t seq = unit / p.blocks, blk = unit % p.blocks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / kLanes, l = lane % kLanes;
-  int64_t c0 = blk * TileT::kChannels + (kVec ? 2 * l : l);
-  const bool in0 = c0 < p.d, in1 = c0 + (kVec ? 1 : kLanes) < p.d;
-  const int next = kVec ? 1 : (in1 ? kLanes : 0);
+  // (single binary32 channels of a thread lie kLanes apart, all others side by side)
+  constexpr int kNext = kMode == kSingle && sizeof(T) == 4 ? kLanes : 1;
+  const int64_t block = blk * TileT::kChannels;  // first channel
+  int64_t c0 = block + (kNext == 1 ? 2 * l : l);
+  const bool in0 = c0 < p.d, in1 = c0 + kNext < p.d;
+  const int next = in1 ? kNext : 0;
   if (!in0) c0 = 0;
+  const int channels = (int)(p.d - block < TileT::kChannels ? p.d - block : TileT::kChannels);
   int64_t end = p.L;
   if (p.lengths) {
     const int64_t n = p.lengths[seq];
     end = n < 0 ? 0 : (n < p.L ? n : p.L);
   }
-  const T* vp = static_cast<const T*>(p.v.p) + seq * p.v.bs + c0;
-  const T* gp = static_cast<const T*>(p.g.p) + seq * p.g.bs + c0;
-  const T* zp = kGate ? static_cast<const T*>(p.z.p) + seq * p.z.bs + c0 : nullptr;
+  using St = ScanStage<T, kMode, kLanes, kGate>;
+  const int64_t cin = St::kWords ? block : c0;  // where the copies of inputs start
+  const T* vp = static_cast<const T*>(p.v.p) + seq * p.v.bs + cin;
+  const T* gp = static_cast<const T*>(p.g.p) + seq * p.g.bs + cin;
+  const T* zp = kGate ? static_cast<const T*>(p.z.p) + seq * p.z.bs + cin : nullptr;
   T* yp = static_cast<T*>(p.y.p) + seq * p.y.bs + c0;
   const int64_t first = (int64_t)(warp * TileT::kSubs + sub) * kSteps;
 
@@ -69,9 +75,11 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T
 
   extern __shared__ __align__(128) uint8_t slots[];
   constexpr int kTensors = kGate ? 3 : 2;
-  using St = ScanStage<T, kMode, kLanes, kGate>;
   constexpr int kAhead = St::kBufs - 1;  // rounds fetched ahead
-  const St stage(slots);
+  St stage(slots);
+  stage.rows_at(0, gp, p.g.rs);
+  stage.rows_at(1, vp, p.v.rs);
+  if constexpr (kGate) stage.rows_at(2, zp, p.z.rs);
   __shared__ uint64_t full[St::kBufs];
   const int64_t rounds = (p.tiles + size - 1) / size;
   uint32_t flags = 0;
@@ -92,9 +100,9 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T
     } else {
       const int64_t t0 = (k * size + rank) * TileT::kLen + first;
       const int left = rows_left(end, t0, kSteps);
-      stage.fetch(buf, 0, gp + t0 * p.g.rs, p.g.rs, next, left);
-      stage.fetch(buf, 1, vp + t0 * p.v.rs, p.v.rs, next, left);
-      if constexpr (kGate) stage.fetch(buf, 2, zp + t0 * p.z.rs, p.z.rs, next, left);
+      stage.fetch(buf, 0, gp + t0 * p.g.rs, p.g.rs, next, channels, left);
+      stage.fetch(buf, 1, vp + t0 * p.v.rs, p.v.rs, next, channels, left);
+      if constexpr (kGate) stage.fetch(buf, 2, zp + t0 * p.z.rs, p.z.rs, next, channels, left);
       St::commit();
     }
   };
@@ -111,6 +119,7 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T
       if (!tc::mbar_wait(full + buf, (uint32_t)(k / St::kBufs) & 1u, kWaitLimit))
         flags |= SSMQ_DEV_TIMEOUT;
     } else {
+      St::leave();
       fetch(k + kAhead);
       St::wait();
     }

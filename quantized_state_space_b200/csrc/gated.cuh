@@ -28,7 +28,8 @@ constexpr uint32_t kWaitLimit = 1u << 20;
 enum {
   kTma = 0,    // whole tiles by TMA: rows on 16-byte boundaries
   kPairs = 1,  // each thread its own pairs of channels
-  kSingle = 2  // each thread its own channels one by one
+  kSingle = 2  // rows on any element: 32-bit channels one by one, 16-bit ones as the
+               // aligned words they lie in, shared by the lanes of a row
 };
 
 template <int kWarps_, int kSteps_, int kLanes_>
@@ -57,8 +58,8 @@ struct Rows {
 };
 inline Rows rows_of(const ssmq_rows& r) { return Rows{r.p, r.batch_stride, r.row_stride}; }
 
-// two channels of one row: a pair of consecutive elements (kVec), or elements
-// kLanes apart
+// two channels of one row: consecutive ones, or (single binary32 channels) kLanes
+// apart
 template <typename T>
 struct Pair {
   uint32_t w;
@@ -96,30 +97,53 @@ struct Maps {
 // of the round that reads them, so that no register holds a load in flight.
 // kTma: one thread fetches whole tiles ([row][channel]); rows and channels
 // beyond the tensor read as zero.  Otherwise every thread copies the pairs of
-// its own steps into slots of its own ([step][thread]).  Either way a thread
-// reads only its own steps and channels.
+// its own steps into slots of its own ([step][thread]), or the lanes of a row its
+// words together ([step][row group][word]).  Either way a thread reads only its
+// own steps and channels.
 template <typename T, int kTensors, int kMode, typename TileT, int kBufs_>
 struct Stage {
   static constexpr int kThreads = TileT::kThreads, kSteps = TileT::kSteps;
   static constexpr int kBufs = kBufs_;
-  static constexpr int kTensorBytes = TileT::kLen * TileT::kChannels * (int)sizeof(T);
-  static constexpr int kStepBytes =
-      (kMode == kTma ? TileT::kChannels : 2 * kThreads) * (int)sizeof(T);
+  static constexpr int kLanes = TileT::kLanes;
+  // 16-bit rows on any element: a row's kLanes + 1 words hold its 2 kLanes channels
+  // from either half of the first word on
+  static constexpr bool kWords = kMode == kSingle && sizeof(T) == 2;
+  static constexpr int kStepBytes = kMode == kTma ? TileT::kChannels * (int)sizeof(T)
+                                    : kWords      ? kThreads / kLanes * (kLanes + 1) * 4
+                                                  : 2 * kThreads * (int)sizeof(T);
+  static constexpr int kTensorBytes = (kMode == kTma ? TileT::kLen : kSteps) * kStepBytes;
   static constexpr int kBytes = kBufs * kTensors * kTensorBytes;
   uint8_t* base;  // of this thread's pairs
+  uint32_t halves[2] = {0, 0};  // kWords: bit j, the half word that even (odd) rows of tensor j
+                                // start in (segments start at even rows)
   __device__ __forceinline__ explicit Stage(uint8_t* smem) {
+    const int lane = threadIdx.x & 31;
     if constexpr (kMode == kTma) {
-      const int lane = threadIdx.x & 31;
-      const int row = ((int)(threadIdx.x >> 5) * TileT::kSubs + lane / TileT::kLanes) * kSteps;
-      base = smem + row * kStepBytes + (lane % TileT::kLanes) * 2 * (int)sizeof(T);
+      const int row = ((int)(threadIdx.x >> 5) * TileT::kSubs + lane / kLanes) * kSteps;
+      base = smem + row * kStepBytes + (lane % kLanes) * 2 * (int)sizeof(T);
+    } else if constexpr (kWords) {
+      base = smem + ((int)threadIdx.x / kLanes * (kLanes + 1) + lane % kLanes) * 4;
     } else {
       base = smem + threadIdx.x * 2 * (int)sizeof(T);
+    }
+  }
+  // kWords: where the rows of a tensor start (p: its channel block's first row)
+  __device__ __forceinline__ void rows_at(int tensor, const T* p, int64_t rs) {
+    if constexpr (kWords) {
+      const uint32_t even = (uint32_t)(reinterpret_cast<uintptr_t>(p) >> 1) & 1u;
+      halves[0] |= even << tensor;
+      halves[1] |= (even ^ ((uint32_t)rs & 1u)) << tensor;
     }
   }
   __device__ __forceinline__ uint8_t* at(int buf, int tensor) const {
     return base + (buf * kTensors + tensor) * kTensorBytes;
   }
   __device__ __forceinline__ float2 get(int buf, int tensor, int i) const {
+    if constexpr (kWords) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(at(buf, tensor) + i * kStepBytes);
+      const uint32_t half = (halves[i & 1] >> tensor) & 1u;
+      return pair_f32<T>(Pair<T>{__funnelshift_r(w[0], w[1], 16 * half)});
+    }
     return pair_f32<T>(*reinterpret_cast<const Pair<T>*>(at(buf, tensor) + i * kStepBytes));
   }
   // kTma: the tile at (channel c, step t, sequence s) of one tensor
@@ -134,14 +158,26 @@ struct Stage {
         : "memory");
   }
   // the other modes: rows 0 .. left - 1 of the thread's steps, zeros behind
-  // them.  Lanes without a channel have their pointers clamped to channel 0.
+  // them.  p: the thread's first channel (lanes without one have it clamped to
+  // channel 0), for kWords the block's, of which `channels` exist.
   __device__ __forceinline__ void fetch(int buf, int tensor, const T* p, int64_t rs, int next,
-                                        int left) const {
-    uint8_t* o = at(buf, tensor);
-    if constexpr (kMode == kPairs || sizeof(T) == 4) {
+                                        int channels, int left) const {
+    const uint32_t dst = tc::smem_u32(at(buf, tensor));
+    if constexpr (kWords) {
+      // words that hold a channel of the row (and the one beside it: the word lies
+      // in the tensor's own memory)
+      const int l = (int)threadIdx.x % kLanes;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int half = (int)(halves[i & 1] >> tensor) & 1;
+        const T* src = p + i * rs - half + 2 * l;
+        copy4(dst + i * kStepBytes, src, i < left && 2 * l - half < channels);
+        if (l == kLanes - 1)
+          copy4(dst + i * kStepBytes + 4, src + 2, i < left && 2 * kLanes - half < channels);
+      }
+    } else {
       constexpr int kN = kMode == kPairs ? 1 : 2;  // copies per pair
       constexpr int kCopy = 2 * (int)sizeof(T) / kN;
-      const uint32_t dst = tc::smem_u32(o);
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
         const int bytes = i < left ? kCopy : 0;
@@ -152,17 +188,13 @@ struct Stage {
                        "l"(p + i * rs + j * next), "n"(kCopy), "r"(bytes)
                        : "memory");
       }
-    } else {
-      uint32_t r[kSteps];
-      const uint16_t* u = reinterpret_cast<const uint16_t*>(p);
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        r[i] = 0;
-        if (i < left) r[i] = (uint32_t)u[i * rs] | ((uint32_t)u[i * rs + next] << 16);
-      }
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i) *reinterpret_cast<uint32_t*>(o + i * kStepBytes) = r[i];
     }
+  }
+  // four bytes, or (nothing read) zeros
+  static __device__ __forceinline__ void copy4(uint32_t dst, const T* src, bool on) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+                 "r"(on ? 4 : 0)
+                 : "memory");
   }
   // zeros in the thread's steps from `left` on: tiles by TMA bring the rows
   // behind a sequence's end, and no tile brings those in front of its start
@@ -179,6 +211,11 @@ struct Stage {
   // all but the newest kBufs - 1 groups have landed
   static __device__ __forceinline__ void wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kBufs - 1) : "memory");
+    if constexpr (kWords) __syncwarp();  // (the row's other lanes' words too)
+  }
+  // kWords: the row's lanes have read a slot that is filled next
+  static __device__ __forceinline__ void leave() {
+    if constexpr (kWords) __syncwarp();
   }
 };
 // rows of the segment at t0 that lie before the end, at most `steps`

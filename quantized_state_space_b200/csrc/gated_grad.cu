@@ -48,19 +48,25 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kGradCtas)
   const int64_t seq = unit / p.blocks, blk = unit % p.blocks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / kLanes, l = lane % kLanes;
-  int64_t c0 = blk * TileT::kChannels + (kVec ? 2 * l : l);
-  const bool in0 = c0 < p.d, in1 = c0 + (kVec ? 1 : kLanes) < p.d;
-  const int next = kVec ? 1 : (in1 ? kLanes : 0);
+  // (single binary32 channels of a thread lie kLanes apart, all others side by side)
+  constexpr int kNext = kMode == kSingle && sizeof(T) == 4 ? kLanes : 1;
+  const int64_t block = blk * TileT::kChannels;  // first channel
+  int64_t c0 = block + (kNext == 1 ? 2 * l : l);
+  const bool in0 = c0 < p.d, in1 = c0 + kNext < p.d;
+  const int next = in1 ? kNext : 0;
   if (!in0) c0 = 0;
+  const int channels = (int)(p.d - block < TileT::kChannels ? p.d - block : TileT::kChannels);
   int64_t end = p.L;
   if (p.lengths) {
     const int64_t n = p.lengths[seq];
     end = n < 0 ? 0 : (n < p.L ? n : p.L);
   }
-  const T* vp = static_cast<const T*>(p.v.p) + seq * p.v.bs + c0;
-  const T* gp = static_cast<const T*>(p.g.p) + seq * p.g.bs + c0;
-  const T* zp = kGate ? static_cast<const T*>(p.z.p) + seq * p.z.bs + c0 : nullptr;
-  const T* dyp = static_cast<const T*>(p.dy.p) + seq * p.dy.bs + c0;
+  using St = GradStage<T, kMode, kLanes, kGate>;
+  const int64_t cin = St::kWords ? block : c0;  // where the copies of inputs start
+  const T* vp = static_cast<const T*>(p.v.p) + seq * p.v.bs + cin;
+  const T* gp = static_cast<const T*>(p.g.p) + seq * p.g.bs + cin;
+  const T* zp = kGate ? static_cast<const T*>(p.z.p) + seq * p.z.bs + cin : nullptr;
+  const T* dyp = static_cast<const T*>(p.dy.p) + seq * p.dy.bs + cin;
   T* dvp = static_cast<T*>(p.dv.p) + seq * p.dv.bs + c0;
   T* dgp = static_cast<T*>(p.dg.p) + seq * p.dg.bs + c0;
   T* dzp = kGate ? static_cast<T*>(p.dz.p) + seq * p.dz.bs + c0 : nullptr;
@@ -71,8 +77,11 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kGradCtas)
     c = make_float2(p.dh_final[seq * p.d + c0], p.dh_final[seq * p.d + c0 + next]);
 
   extern __shared__ __align__(128) uint8_t slots[];
-  using St = GradStage<T, kMode, kLanes, kGate>;
-  const St stage(slots);
+  St stage(slots);
+  stage.rows_at(0, gp, p.g.rs);
+  stage.rows_at(1, vp, p.v.rs);
+  stage.rows_at(2, dyp, p.dy.rs);
+  if constexpr (kGate) stage.rows_at(3, zp, p.z.rs);
   __shared__ uint64_t full[St::kBufs];
   const int64_t rounds = (p.tiles + size - 1) / size;
   uint32_t flags = 0;
@@ -93,10 +102,10 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kGradCtas)
       if (k < rounds) {
         const int64_t t0 = tile >= 0 ? tile * TileT::kLen + first : 0;
         const int left = tile >= 0 ? rows_left(end, t0, kSteps) : 0;
-        stage.fetch(buf, 0, gp + t0 * p.g.rs, p.g.rs, next, left);
-        stage.fetch(buf, 1, vp + t0 * p.v.rs, p.v.rs, next, left);
-        stage.fetch(buf, 2, dyp + t0 * p.dy.rs, p.dy.rs, next, left);
-        if constexpr (kGate) stage.fetch(buf, 3, zp + t0 * p.z.rs, p.z.rs, next, left);
+        stage.fetch(buf, 0, gp + t0 * p.g.rs, p.g.rs, next, channels, left);
+        stage.fetch(buf, 1, vp + t0 * p.v.rs, p.v.rs, next, channels, left);
+        stage.fetch(buf, 2, dyp + t0 * p.dy.rs, p.dy.rs, next, channels, left);
+        if constexpr (kGate) stage.fetch(buf, 3, zp + t0 * p.z.rs, p.z.rs, next, channels, left);
       }
       St::commit();
     }
