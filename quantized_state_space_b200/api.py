@@ -885,7 +885,8 @@ def gated_scan(v, g, *, z=None, h0=None, lengths=None, y=None, h_final=None, sta
     h_final, states) with save_states: the states that gated_scan_backward
     reads (or that are written into ``states`` when it is given).  When an
     input requires a gradient, the result is differentiable; the caller's
-    output tensors are then not accepted."""
+    output tensors are then not accepted.  (To capture a training step in a
+    CUDA graph, call gated_scan with save_states and gated_scan_backward.)"""
     if torch.is_grad_enabled() and (v.requires_grad or g.requires_grad or
                                     (z is not None and z.requires_grad) or
                                     (h0 is not None and h0.requires_grad)):

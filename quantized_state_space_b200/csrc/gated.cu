@@ -18,12 +18,14 @@ using namespace gated;
 template <typename T, int kMode>
 constexpr int kScanCtas = kMode == kTma ? 3 : (sizeof(T) == 4 ? 2 : 3);
 // A tile by TMA is fetched into the buffer of the round before the current one;
-// gated binary32 copied by the threads takes one buffer (two leave room for one CTA
-// per SM: 369 us against 278 at 1 x 12798 x 4394).
+// what the threads copy takes one buffer (gated binary32: two, which leave room for
+// one CTA per SM, took 369 us against 278 at 1 x 12798 x 4394; binary16 pairs: 70
+// against 66 at 8 x 2048 x 1538), ungated binary32 two (92 against 98 at
+// 52 x 233 x 2717).
 template <typename T, int kMode, int kLanes, bool kGate>
 using ScanStage = Stage<T, kGate ? 3 : 2, kMode, ModeTile<kMode, kLanes>,
                         kMode == kTma ? (sizeof(T) == 2 && !kGate ? 3 : 2)
-                                      : (sizeof(T) == 2 || !kGate ? 2 : 1)>;
+                                      : (sizeof(T) == 4 && !kGate ? 2 : 1), true>;
 
 struct ScanParams {
   int64_t L, d, blocks;
@@ -49,8 +51,8 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T
   const int64_t seq = unit / p.blocks, blk = unit % p.blocks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / kLanes, l = lane % kLanes;
-  // (single binary32 channels of a thread lie kLanes apart, all others side by side)
-  constexpr int kNext = kMode == kSingle && sizeof(T) == 4 ? kLanes : 1;
+  using St = ScanStage<T, kMode, kLanes, kGate>;
+  constexpr int kNext = St::kNext;
   const int64_t block = blk * TileT::kChannels;  // first channel
   int64_t c0 = block + (kNext == 1 ? 2 * l : l);
   const bool in0 = c0 < p.d, in1 = c0 + kNext < p.d;
@@ -62,7 +64,6 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T
     const int64_t n = p.lengths[seq];
     end = n < 0 ? 0 : (n < p.L ? n : p.L);
   }
-  using St = ScanStage<T, kMode, kLanes, kGate>;
   const int64_t cin = St::kWords ? block : c0;  // where the copies of inputs start
   const T* vp = static_cast<const T*>(p.v.p) + seq * p.v.bs + cin;
   const T* gp = static_cast<const T*>(p.g.p) + seq * p.g.bs + cin;

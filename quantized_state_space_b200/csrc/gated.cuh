@@ -28,8 +28,8 @@ constexpr uint32_t kWaitLimit = 1u << 20;
 enum {
   kTma = 0,    // whole tiles by TMA: rows on 16-byte boundaries
   kPairs = 1,  // each thread its own pairs of channels
-  kSingle = 2  // rows on any element: 32-bit channels one by one, 16-bit ones as the
-               // aligned words they lie in, shared by the lanes of a row
+  kSingle = 2  // rows on any element: its own channels one by one, or 16-bit ones as
+               // the aligned words they lie in, shared by the lanes of a row
 };
 
 template <int kWarps_, int kSteps_, int kLanes_>
@@ -58,8 +58,7 @@ struct Rows {
 };
 inline Rows rows_of(const ssmq_rows& r) { return Rows{r.p, r.batch_stride, r.row_stride}; }
 
-// two channels of one row: consecutive ones, or (single binary32 channels) kLanes
-// apart
+// two channels of one row
 template <typename T>
 struct Pair {
   uint32_t w;
@@ -99,15 +98,20 @@ struct Maps {
 // beyond the tensor read as zero.  Otherwise every thread copies the pairs of
 // its own steps into slots of its own ([step][thread]), or the lanes of a row its
 // words together ([step][row group][word]).  Either way a thread reads only its
-// own steps and channels.
-template <typename T, int kTensors, int kMode, typename TileT, int kBufs_>
+// own steps and channels.  kDirect: copies of 16-bit channels and of pairs go
+// through registers, not as asynchronous copies of 4 bytes, which the forward kernel
+// with its many warps does not need (8 x 2048 x 1538 binary16, gated: 108 us against
+// 72; odd rows, 1537: 108 against 84; the gradient's odd rows: 188 against 234).
+template <typename T, int kTensors, int kMode, typename TileT, int kBufs_, bool kDirect>
 struct Stage {
   static constexpr int kThreads = TileT::kThreads, kSteps = TileT::kSteps;
   static constexpr int kBufs = kBufs_;
   static constexpr int kLanes = TileT::kLanes;
   // 16-bit rows on any element: a row's kLanes + 1 words hold its 2 kLanes channels
   // from either half of the first word on
-  static constexpr bool kWords = kMode == kSingle && sizeof(T) == 2;
+  static constexpr bool kWords = kMode == kSingle && sizeof(T) == 2 && !kDirect;
+  // channels of a thread's pair: side by side, or kLanes apart
+  static constexpr int kNext = kMode == kSingle && !kWords ? kLanes : 1;
   static constexpr int kStepBytes = kMode == kTma ? TileT::kChannels * (int)sizeof(T)
                                     : kWords      ? kThreads / kLanes * (kLanes + 1) * 4
                                                   : 2 * kThreads * (int)sizeof(T);
@@ -162,6 +166,34 @@ struct Stage {
   // channel 0), for kWords the block's, of which `channels` exist.
   __device__ __forceinline__ void fetch(int buf, int tensor, const T* p, int64_t rs, int next,
                                         int channels, int left) const {
+    if constexpr (kDirect && (kMode == kPairs || sizeof(T) == 2)) {
+      uint8_t* o = at(buf, tensor);
+      Pair<T> r[kSteps];
+      if constexpr (kMode == kPairs) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const T* src = p + i * rs;
+          r[i] = Pair<T>{};
+          if (i < left && channels > 0) r[i] = *reinterpret_cast<const Pair<T>*>(src);
+        }
+      } else {
+        const uint16_t* u = reinterpret_cast<const uint16_t*>(p);
+        if (left == kSteps) {  // (without branches between the loads)
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i)
+            r[i].w = (uint32_t)u[i * rs] | ((uint32_t)u[i * rs + next] << 16);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            r[i] = Pair<T>{};
+            if (i < left) r[i].w = (uint32_t)u[i * rs] | ((uint32_t)u[i * rs + next] << 16);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) *reinterpret_cast<Pair<T>*>(o + i * kStepBytes) = r[i];
+      return;
+    }
     const uint32_t dst = tc::smem_u32(at(buf, tensor));
     if constexpr (kWords) {
       // words that hold a channel of the row (and the one beside it: the word lies

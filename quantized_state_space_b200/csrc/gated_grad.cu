@@ -22,7 +22,8 @@ using namespace gated;
 constexpr int kGradCtas = 2;  // per SM
 // A round's inputs are read before its exchange: the slot refills behind it.
 template <typename T, int kMode, int kLanes, bool kGate>
-using GradStage = Stage<T, kGate ? 4 : 3, kMode, ModeTile<kMode, kLanes>, sizeof(T) == 2 ? 2 : 1>;
+using GradStage = Stage<T, kGate ? 4 : 3, kMode, ModeTile<kMode, kLanes>, sizeof(T) == 2 ? 2 : 1,
+                        sizeof(T) == 2 && kMode == kPairs>;
 
 struct GradParams {
   int64_t L, d, blocks;
@@ -48,8 +49,8 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kGradCtas)
   const int64_t seq = unit / p.blocks, blk = unit % p.blocks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / kLanes, l = lane % kLanes;
-  // (single binary32 channels of a thread lie kLanes apart, all others side by side)
-  constexpr int kNext = kMode == kSingle && sizeof(T) == 4 ? kLanes : 1;
+  using St = GradStage<T, kMode, kLanes, kGate>;
+  constexpr int kNext = St::kNext;
   const int64_t block = blk * TileT::kChannels;  // first channel
   int64_t c0 = block + (kNext == 1 ? 2 * l : l);
   const bool in0 = c0 < p.d, in1 = c0 + kNext < p.d;
@@ -61,7 +62,6 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kGradCtas)
     const int64_t n = p.lengths[seq];
     end = n < 0 ? 0 : (n < p.L ? n : p.L);
   }
-  using St = GradStage<T, kMode, kLanes, kGate>;
   const int64_t cin = St::kWords ? block : c0;  // where the copies of inputs start
   const T* vp = static_cast<const T*>(p.v.p) + seq * p.v.bs + cin;
   const T* gp = static_cast<const T*>(p.g.p) + seq * p.g.bs + cin;
