@@ -789,7 +789,7 @@ ssmq_status ssmq_int8_linear(const ssmq_linear_args* args, void* workspace, size
  * by subtraction); y and the gradients are rounded once to dtype.  g = -inf
  * forgets the state (f = 0: a new sequence starts), g = +inf keeps it and
  * ignores a finite v.  A non-finite v or state makes the later states of its
- * channel non-finite.
+ * channel non-finite, a NaN g makes them NaN.
  *
  * Layouts (b = batch, L = seqlen, d = dim): v, g, z, y, dy, dv, dg, dz are
  * (b, L, d) of dtype, element (i, t, c) at i * batch_stride + t * row_stride + c
