@@ -785,8 +785,8 @@ ssmq_status ssmq_int8_linear(const ssmq_linear_args* args, void* workspace, size
  *   f_t = sigmoid(g_t),  h_t = f_t h_{t-1} + (1 - f_t) v_t
  *   y_t = h_t             without z
  *   y_t = h_t silu(z_t)   with z
- * Gates, states and sums are binary32 (1 - f_t is formed as sigmoid(-g_t), not
- * by subtraction); y and the gradients are rounded once to dtype.  g = -inf
+ * Gates, states and sums are binary32 (the smaller of f_t and 1 - f_t is formed
+ * directly, the larger as 1 minus it); y and the gradients are rounded once to dtype.  g = -inf
  * forgets the state (f = 0: a new sequence starts), g = +inf keeps it and
  * ignores a finite v.  A non-finite v or state makes the later states of its
  * channel non-finite, a NaN g makes them NaN.

@@ -256,28 +256,22 @@ __device__ __forceinline__ int rows_left(int64_t end, int64_t t0, int steps) {
   return n < 0 ? 0 : (n < steps ? (int)n : steps);
 }
 
-// The smaller of two values; NaN if either is.
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float y;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
-
-// e = exp(-g) with the exponent kept below 2^126, r = 1 / (1 + e): n = 1 - f =
-// e r and, for g < 0, f = r, to a few ulps and the rounding of the exponent
-// (|g| 2^-23); for g >= 0, f is formed as 1 - n (n <= 1/2: half an ulp), not as
-// the approximate reciprocal, whose ulp a long memory would accumulate.  A NaN g
-// makes both NaN.
+// e = exp(-g), r = 1 / (1 + e).  The smaller of f and n = 1 - f is r for g < 0, else
+// e r, to a few ulps and the rounding of the exponent (|g| 2^-23); the larger is 1
+// minus it (at most half an ulp off), not the approximate reciprocal, whose ulp a
+// long memory would accumulate.  g = -inf: e = inf, f = 0, n = 1; a NaN g makes both
+// NaN.
 __device__ __forceinline__ void gate2(float2 g, float2& f, float2& n) {
   const float2 x = fmul2(g, make_float2(-kLog2e, -kLog2e));
-  const float2 e = make_float2(ex2_sfu(min_nan(x.x, 126.0f)), ex2_sfu(min_nan(x.y, 126.0f)));
+  const float2 e = make_float2(ex2_sfu(x.x), ex2_sfu(x.y));
   const float2 one = make_float2(1.0f, 1.0f);
   const float2 d = fadd2(one, e);
   const float2 r = make_float2(rcp_sfu(d.x), rcp_sfu(d.y));
-  n = fmul2(e, r);
-  const float2 c = fsub2(one, n);
-  f.x = g.x < 0.0f ? r.x : c.x;
-  f.y = g.y < 0.0f ? r.y : c.y;
+  const float2 er = fmul2(e, r);  // (g < 0: not used)
+  const float2 not_r = fsub2(one, r), not_er = fsub2(one, er);
+  const bool neg0 = g.x < 0.0f, neg1 = g.y < 0.0f;
+  f = make_float2(neg0 ? r.x : not_er.x, neg1 ? r.y : not_er.y);
+  n = make_float2(neg0 ? not_r.x : er.x, neg1 ? not_r.y : er.y);
 }
 __device__ __forceinline__ float2 sigmoid2(float2 z) {
   const float2 x = fmul2(z, make_float2(-kLog2e, -kLog2e));

@@ -1,6 +1,6 @@
 """Gates at the ends of their range: a NaN logit makes the later states of its
 channel NaN (and the gradients that pass through it), in every kernel of the
-gated recurrence.
+gated recurrence; g = -inf leaves nothing of the state, however large it is.
 
 The comparison counts a NaN on one side alone as a difference.
 """
@@ -93,3 +93,30 @@ def test_nan_behind_a_sequence_is_not_read(size, strided, dtype):
         p["g"][i, n:] = float("nan")
     r, y, h = run_and_agree(p)
     assert torch.isfinite(y).all() and torch.isfinite(h).all()
+
+@pytest.mark.parametrize("size,strided", MODES)
+def test_minus_infinity_leaves_nothing(size, strided):
+    """States beyond 2^100: 2^-126 of them would show."""
+    b, L, d = size
+    p = problem(34, b, L, d, F32, strided=strided)
+    p["h0"].fill_(2.0 ** 126)
+    p["g"][:, 0] = -float("inf")
+    y, h = api.gated_scan(p["v"], p["g"], z=p["z"], h0=p["h0"])
+    assert torch.equal(*(api.gated_scan(p["v"], p["g"], z=p["z"], h0=h0)[0]
+                         for h0 in (p["h0"], None)))
+    r = Ref(p["v"], p["g"], p["z"])
+    agree(r, "y", y)
+    r.h_final_err = r.h_err
+    agree(r, "h_final", h)
+    _, _, st = api.gated_scan(p["v"], p["g"], z=p["z"], h0=p["h0"], save_states=True)
+    grads = api.gated_scan_backward(p["dy"], p["v"], p["g"], st, z=p["z"], dh_final=p["dh"])
+    assert not grads[3].any() and not grads[1][:, 0].any()  # f = 0: nothing reaches h0 or g
+
+
+def test_minus_infinity_leaves_nothing_of_one_state():
+    for d in (16, 33):
+        p = problem(35, 4, 1, d, F32)
+        p["g"].fill_(-float("inf"))
+        state = torch.full((4, d), 2.0 ** 127, device=dev())
+        y = api.gated_update(state, p["v"][:, 0], p["g"][:, 0])
+        assert torch.equal(state, p["v"][:, 0]) and torch.equal(y, p["v"][:, 0])
