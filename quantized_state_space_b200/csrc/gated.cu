@@ -5,8 +5,9 @@
 // channel and the decay as an input.
 //
 // Bound: HBM (v, g, z in, y out).  The inputs are read once: a tile's gates
-// stay in registers while the carried states are exchanged (gated.cuh), and
-// the next round's rows are copied into shared memory meanwhile.
+// stay in registers while the carried states are exchanged (gated.cuh).  Where a
+// tile has two buffers or more (TMA, ungated binary32) the next rounds' rows arrive
+// in shared memory meanwhile; with one buffer a round reads its own rows first.
 #include "gated.cuh"
 
 namespace ssmq {
@@ -53,21 +54,18 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T
   const int sub = lane / kLanes, l = lane % kLanes;
   using St = ScanStage<T, kMode, kLanes, kGate>;
   constexpr int kNext = St::kNext;
-  const int64_t block = blk * TileT::kChannels;  // first channel
-  int64_t c0 = block + (kNext == 1 ? 2 * l : l);
+  int64_t c0 = blk * TileT::kChannels + (kNext == 1 ? 2 * l : l);  // first channel
   const bool in0 = c0 < p.d, in1 = c0 + kNext < p.d;
   const int next = in1 ? kNext : 0;
   if (!in0) c0 = 0;
-  const int channels = (int)(p.d - block < TileT::kChannels ? p.d - block : TileT::kChannels);
   int64_t end = p.L;
   if (p.lengths) {
     const int64_t n = p.lengths[seq];
     end = n < 0 ? 0 : (n < p.L ? n : p.L);
   }
-  const int64_t cin = St::kWords ? block : c0;  // where the copies of inputs start
-  const T* vp = static_cast<const T*>(p.v.p) + seq * p.v.bs + cin;
-  const T* gp = static_cast<const T*>(p.g.p) + seq * p.g.bs + cin;
-  const T* zp = kGate ? static_cast<const T*>(p.z.p) + seq * p.z.bs + cin : nullptr;
+  const T* vp = static_cast<const T*>(p.v.p) + seq * p.v.bs + c0;
+  const T* gp = static_cast<const T*>(p.g.p) + seq * p.g.bs + c0;
+  const T* zp = kGate ? static_cast<const T*>(p.z.p) + seq * p.z.bs + c0 : nullptr;
   T* yp = static_cast<T*>(p.y.p) + seq * p.y.bs + c0;
   const int64_t first = (int64_t)(warp * TileT::kSubs + sub) * kSteps;
 
@@ -78,9 +76,6 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T
   constexpr int kTensors = kGate ? 3 : 2;
   constexpr int kAhead = St::kBufs - 1;  // rounds fetched ahead
   St stage(slots);
-  stage.rows_at(0, gp, p.g.rs);
-  stage.rows_at(1, vp, p.v.rs);
-  if constexpr (kGate) stage.rows_at(2, zp, p.z.rs);
   __shared__ uint64_t full[St::kBufs];
   const int64_t rounds = (p.tiles + size - 1) / size;
   uint32_t flags = 0;
@@ -101,9 +96,9 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T
     } else {
       const int64_t t0 = (k * size + rank) * TileT::kLen + first;
       const int left = rows_left(end, t0, kSteps);
-      stage.fetch(buf, 0, gp + t0 * p.g.rs, p.g.rs, next, channels, left);
-      stage.fetch(buf, 1, vp + t0 * p.v.rs, p.v.rs, next, channels, left);
-      if constexpr (kGate) stage.fetch(buf, 2, zp + t0 * p.z.rs, p.z.rs, next, channels, left);
+      stage.fetch(buf, 0, gp + t0 * p.g.rs, p.g.rs, next, left);
+      stage.fetch(buf, 1, vp + t0 * p.v.rs, p.v.rs, next, left);
+      if constexpr (kGate) stage.fetch(buf, 2, zp + t0 * p.z.rs, p.z.rs, next, left);
       St::commit();
     }
   };
@@ -120,7 +115,6 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T
       if (!tc::mbar_wait(full + buf, (uint32_t)(k / St::kBufs) & 1u, kWaitLimit))
         flags |= SSMQ_DEV_TIMEOUT;
     } else {
-      St::leave();
       fetch(k + kAhead);
       St::wait();
     }
@@ -189,6 +183,7 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T
 
 template <typename T>
 cudaError_t scan_type(const ssmq_gated_args& a, cudaStream_t st) {
+  // (three CTAs an SM for every type and mode: what 16-bit types by TMA hold)
   const Shape s = shape_for(a.batch, a.seqlen, a.dim, 3 * (int64_t)sm_count(), 1);
   const int len = s.narrow ? kNarrowLen : kWideLen;
   ScanParams p;

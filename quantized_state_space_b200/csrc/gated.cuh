@@ -120,6 +120,7 @@ struct Stage {
   uint8_t* base;  // of this thread's pairs
   uint32_t halves[2] = {0, 0};  // kWords: bit j, the half word that even (odd) rows of tensor j
                                 // start in (segments start at even rows)
+  int channels = 0;             // kWords: channels of the block
   __device__ __forceinline__ explicit Stage(uint8_t* smem) {
     const int lane = threadIdx.x & 31;
     if constexpr (kMode == kTma) {
@@ -163,9 +164,9 @@ struct Stage {
   }
   // the other modes: rows 0 .. left - 1 of the thread's steps, zeros behind
   // them.  p: the thread's first channel (lanes without one have it clamped to
-  // channel 0), for kWords the block's, of which `channels` exist.
+  // channel 0), for kWords the block's.
   __device__ __forceinline__ void fetch(int buf, int tensor, const T* p, int64_t rs, int next,
-                                        int channels, int left) const {
+                                        int left) const {
     if constexpr (kDirect && (kMode == kPairs || sizeof(T) == 2)) {
       uint8_t* o = at(buf, tensor);
       Pair<T> r[kSteps];
@@ -174,7 +175,7 @@ struct Stage {
         for (int i = 0; i < kSteps; ++i) {
           const T* src = p + i * rs;
           r[i] = Pair<T>{};
-          if (i < left && channels > 0) r[i] = *reinterpret_cast<const Pair<T>*>(src);
+          if (i < left) r[i] = *reinterpret_cast<const Pair<T>*>(src);
         }
       } else {
         const uint16_t* u = reinterpret_cast<const uint16_t*>(p);
@@ -244,10 +245,6 @@ struct Stage {
   static __device__ __forceinline__ void wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kBufs - 1) : "memory");
     if constexpr (kWords) __syncwarp();  // (the row's other lanes' words too)
-  }
-  // kWords: the row's lanes have read a slot that is filled next
-  static __device__ __forceinline__ void leave() {
-    if constexpr (kWords) __syncwarp();
   }
 };
 // rows of the segment at t0 that lie before the end, at most `steps`

@@ -9,9 +9,10 @@
 // forward map.
 //
 // Bound: HBM (v, g, z, dy in, dv, dg, dz out).  A tile's gates stay in
-// registers and its inputs in shared memory (copied one round ahead): the forward states inside it are rebuilt from the state that the
-// forward call saved at its start (one per 64 steps), so neither h nor the
-// gates cross memory, and only c travels between the CTAs of a cluster.
+// registers and its inputs in shared memory (copied one round ahead): the forward
+// states inside it are rebuilt from the state that the forward call saved at its
+// start (one per 64 steps), so neither h nor the gates cross memory, and only c
+// travels between the CTAs of a cluster.
 #include "gated.cuh"
 
 namespace ssmq {
@@ -56,7 +57,6 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kGradCtas)
   const bool in0 = c0 < p.d, in1 = c0 + kNext < p.d;
   const int next = in1 ? kNext : 0;
   if (!in0) c0 = 0;
-  const int channels = (int)(p.d - block < TileT::kChannels ? p.d - block : TileT::kChannels);
   int64_t end = p.L;
   if (p.lengths) {
     const int64_t n = p.lengths[seq];
@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kGradCtas)
   stage.rows_at(1, vp, p.v.rs);
   stage.rows_at(2, dyp, p.dy.rs);
   if constexpr (kGate) stage.rows_at(3, zp, p.z.rs);
+  stage.channels = (int)(p.d - block < TileT::kChannels ? p.d - block : TileT::kChannels);
   __shared__ uint64_t full[St::kBufs];
   const int64_t rounds = (p.tiles + size - 1) / size;
   uint32_t flags = 0;
@@ -102,10 +103,10 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kGradCtas)
       if (k < rounds) {
         const int64_t t0 = tile >= 0 ? tile * TileT::kLen + first : 0;
         const int left = tile >= 0 ? rows_left(end, t0, kSteps) : 0;
-        stage.fetch(buf, 0, gp + t0 * p.g.rs, p.g.rs, next, channels, left);
-        stage.fetch(buf, 1, vp + t0 * p.v.rs, p.v.rs, next, channels, left);
-        stage.fetch(buf, 2, dyp + t0 * p.dy.rs, p.dy.rs, next, channels, left);
-        if constexpr (kGate) stage.fetch(buf, 3, zp + t0 * p.z.rs, p.z.rs, next, channels, left);
+        stage.fetch(buf, 0, gp + t0 * p.g.rs, p.g.rs, next, left);
+        stage.fetch(buf, 1, vp + t0 * p.v.rs, p.v.rs, next, left);
+        stage.fetch(buf, 2, dyp + t0 * p.dy.rs, p.dy.rs, next, left);
+        if constexpr (kGate) stage.fetch(buf, 3, zp + t0 * p.z.rs, p.z.rs, next, left);
       }
       St::commit();
     }
