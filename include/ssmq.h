@@ -73,7 +73,8 @@ typedef enum {
                                  wait probes at most ~2^20 times (about a second).
                                  For tests of this path, the environment variable
                                  SSMQ_WAIT_LIMIT=<probes> (read at each call) lowers
-                                 the limit of ssmq_quantize_groups' pipeline waits;
+                                 the limit of the waits for copies in
+                                 ssmq_quantize_groups and ssmq_int8_linear;
                                  0 makes them give up at once. */
 
 typedef enum {
@@ -751,7 +752,8 @@ ssmq_status ssmq_rms_norm_quantize(const ssmq_norm_args* args, void* stream);
  *              such rows.  One call at a time per workspace.
  * in_features == 0 gives the bias.  Supported: in_features <= 131071 (the
  * sums stay inside 32 bits for every code, -128 among them).
- * status: SSMQ_DEV_TIMEOUT if a bounded device wait gave up.
+ * status: SSMQ_DEV_TIMEOUT if a bounded device wait gave up; what such a call did
+ * not finish of y is NaN.
  * Errors: INVALID_ARG (NULL, sizes, strides, overlaps, workspace), UNSUPPORTED
  * (in_features, more than 2^31 - 1 tokens or channels), ALIGNMENT.
  */

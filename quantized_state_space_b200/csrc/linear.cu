@@ -42,6 +42,10 @@ struct LinParams {
   uint32_t* status;
   int64_t tok_tiles, ch_tiles, group;  // persistent kernel: tile order
   bool tma_out;                        // and whether y goes out by TMA
+  // probes before a wait of the copies' or the epilogue's threads gives up (the MMA
+  // thread's waits keep kWaitLimit: with a limit from memory its loop is slower, 145.5
+  // against 140.5 us at 16384 x 2560 x 5120)
+  uint32_t wait_limit;
 };
 
 // ---- PTX ---------------------------------------------------------------------
@@ -114,6 +118,32 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
       "[%0], %1;" ::"r"(tc::smem_u32(bar)),
       "h"((uint16_t)3)
       : "memory");
+}
+// what a barrier of this CTA still expects, less `bytes` that will not come
+__device__ __forceinline__ void complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(
+                   tc::smem_u32(bar)),
+               "r"(bytes)
+               : "memory");
+}
+// a word of another CTA's shared memory (an address from mapa)
+__device__ __forceinline__ void store_remote(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void store_remote64(uint32_t addr, int64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+// whether `ok` holds in all `n` threads that meet at named barrier `id`
+__device__ __forceinline__ bool all_of(uint32_t id, uint32_t n, bool ok) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.and.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
 }
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
@@ -210,6 +240,23 @@ __device__ __forceinline__ void store_any(const LinParams& p, const Channel& c, 
     store_tokens<__nv_bfloat16>(p, c, t0, xs, acc);
   else
     store_tokens<float>(p, c, t0, xs, acc);
+}
+// NaN for `n` tokens from t0 of this lane's channel: the outputs that a call whose
+// wait gave up does not finish
+__device__ __forceinline__ void poison_tokens(const LinParams& p, const Channel& c, int64_t t0,
+                                              int n) {
+  const float nan = __int_as_float(0x7fffffff);
+#pragma unroll 1
+  for (int i = 0; i < n && t0 + i < p.M; ++i) {
+    const int64_t at = (t0 + i) * p.ldy + c.n;
+    if (!c.in) continue;
+    if (p.dtype == SSMQ_F16)
+      static_cast<__half*>(p.y)[at] = from_f32<__half>(nan);
+    else if (p.dtype == SSMQ_BF16)
+      static_cast<__nv_bfloat16*>(p.y)[at] = from_f32<__nv_bfloat16>(nan);
+    else
+      static_cast<float*>(p.y)[at] = nan;
+  }
 }
 // The same values into a shared-memory tile [token][128 channels], at this lane's
 // channel.
@@ -424,6 +471,10 @@ __global__ void __launch_bounds__(kSplitThreads)
 // so eight warps per CTA write tile i (through shared memory by TMA, 256-byte rows,
 // where y lies on 16-byte rows) while the MMAs of tile i + 1 run (four were
 // slower than the MMAs: 206 against 126 us of MMAs at 16384 x 2560 x 5120).
+// A wait that gives up raises a word in both CTAs.  Each role then ends by itself (no
+// accumulator is handed on that is not complete), the epilogue writes NaN to the tiles
+// it has left, and behind the pair's last barrier the copies and MMAs in flight are
+// waited for, before shared and tensor memory go.
 constexpr int kPairThreads = 384;  // warp 0 TMA, 1 MMA, 2 TMEM, 4-11 epilogue
 constexpr int kPairStages = 5;  // (4 to 7 measured the same)
 constexpr int kPairStage = 2 * kOperand;
@@ -457,8 +508,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
   uint64_t* empty = full + kPairStages;
   uint64_t* acc_full = empty + kPairStages;  // [2]
   uint64_t* acc_empty = acc_full + 2;        // [2], the leader's collect both CTAs
-  uint32_t* slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  uint64_t* idle = acc_empty + 2;            // after a wait gave up: the MMAs are done
+  uint32_t* slot = reinterpret_cast<uint32_t*>(idle + 1);
   volatile uint32_t* gave_up = slot + 1;
+  // the leader's: stages filled by the other CTA
+  volatile int64_t* other_uses = reinterpret_cast<volatile int64_t*>(slot + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cta_rank();
@@ -474,6 +528,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
       tc::mbar_init(acc_full + i, 1);
       tc::mbar_init(acc_empty + i, 2 * 8);  // the epilogue warps of both CTAs
     }
+    tc::mbar_init(idle, 1);
     *gave_up = 0;
   }
   if (warp == 2) {
@@ -486,7 +541,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
   cluster_sync();  // barriers of both CTAs exist
   tc::fence_after();
   const uint32_t tmem = *slot;
+  auto give_up = [&] {  // (after the barrier above: the other CTA's word is set up)
+    *gave_up = 1;
+    store_remote(mapa(tc::smem_u32(slot + 1), rank ^ 1u), 1u);
+  };
 
+  int64_t uses = 0;  // stages filled by this CTA
   if (warp == 0 && lane == 0) {
     prefetch_map(&wmap);
     prefetch_map(&xmap);
@@ -500,7 +560,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
       for (int kb = 0; kb < p.kblocks; ++kb, ++i) {
         const int s = (int)(i % kPairStages);
         if (i >= kPairStages &&
-            !tc::mbar_wait(empty + s, (uint32_t)(i / kPairStages - 1) & 1u, kWaitLimit)) {
+            !tc::mbar_wait(empty + s, (uint32_t)(i / kPairStages - 1) & 1u, p.wait_limit)) {
           ok = false;
           break;
         }
@@ -511,18 +571,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
         tma_load_pair(dst + kOperand, &xmap, kb * kBlockK, xrow, bar);
       }
     }
-    if (!ok) {
-      *gave_up = 1;
-      if (rank == 0)  // copies in flight land before the CTAs leave
-        for (int64_t j = i > kPairStages ? i - kPairStages : 0; j < i; ++j)
-          tc::mbar_wait(full + j % kPairStages, (uint32_t)(j / kPairStages) & 1u, kWaitLimit);
-    }
+    if (!ok) give_up();
+    uses = i;
+    if (rank == 1) store_remote64(mapa(tc::smem_u32(const_cast<int64_t*>(other_uses)), 0), uses);
   } else if (warp == 1 && lane == 0 && rank == 0) {
     constexpr uint32_t idesc = idesc_i8(kPairCh, kPairTok);
     int64_t i = 0;
     int64_t n = 0;  // tiles of this pair
     bool ok = true;
-    for (int64_t t = pair; t < tiles && ok; t += pairs, ++n) {
+    for (int64_t t = pair; t < tiles; t += pairs, ++n) {
       const int b = (int)(n & 1);
       if (n >= 2 && !tc::mbar_wait(acc_empty + b, (uint32_t)(n / 2 - 1) & 1u, kWaitLimit)) {
         ok = false;
@@ -544,14 +601,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
           mma_i8<2>(d, ad + 2 * q, bd + 2 * q, idesc, kb > 0 || q > 0);
         commit_pair(empty + s);
       }
+      if (!ok) break;
       commit_pair(acc_full + b);
     }
-    if (!ok) *gave_up = 1;
+    if (!ok) give_up();
   } else if (warp >= 4) {
     const int quarter = warp & 3;                  // TMEM lanes that the warp may read
     const int half = (warp - 4) / 4 * (kPairTok / 2);  // its token columns
-    int64_t n = 0;
-    for (int64_t t = pair; t < tiles; t += pairs, ++n) {
+    const uint32_t half_bar = 1 + (warp - 4) / 4;  // the half's four warps meet here
+    const bool one = quarter == 0 && lane == 0;    // issues the half's stores
+    int64_t n = 0, t = pair;
+    for (; t < tiles; t += pairs, ++n) {
       const int b = (int)(n & 1);
       int64_t ch, tok;
       tile_at(p, t, ch, tok);
@@ -560,27 +620,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
       float xs[kPairTok / 64];
 #pragma unroll
       for (int q = 0; q < kPairTok / 64; ++q) xs[q] = token_scale(p, t0 + 32 * q, 32);
-      const bool ok = tc::mbar_wait(acc_full + b, (uint32_t)(n / 2) & 1u, kWaitLimit);
-      if (!__all_sync(0xFFFFFFFFu, ok)) {
-        *gave_up = 1;
+      // the half's warps go on together (they meet again below), and its staging is
+      // free then; without staging each warp decides for itself
+      bool ok = tc::mbar_wait(acc_full + b, (uint32_t)(n / 2) & 1u, p.wait_limit);
+      if (p.tma_out) {
+        if (one) tma_stores_read();
+        ok = all_of(half_bar, 128, ok);
+      } else {
+        ok = __all_sync(0xFFFFFFFFu, ok);
+      }
+      if (!ok) {
+        if (lane == 0) give_up();
         break;
       }
       tc::fence_after();
       const uint32_t src = tmem + (uint32_t)(b * kPairTok + half) + ((uint32_t)(quarter * 32) << 16);
       const uint32_t at = tc::smem_u32(out + (warp - 4) / 4 * kHalfStage);
-      const bool one = quarter == 0 && lane == 0;  // issues the half's stores
       const int64_t ch0 = ch * kPairCh + rank * kRows;
-      // the half's four warps meet: its staging is free, or (after) complete
-      auto free_stage = [&] {
-        if (one) tma_stores_read();
-        tc::named_sync(1 + (warp - 4) / 4, 128);
-      };
+      // the half's four warps meet: its staging is complete
       auto send_stage = [&](int64_t tok0) {
         tc::fence_async_smem();
-        tc::named_sync(1 + (warp - 4) / 4, 128);
+        tc::named_sync(half_bar, 128);
         if (one && ch0 < p.N && tok0 < p.M) tma_store(&ymap, at, (int)ch0, (int)tok0);
       };
-      if (p.tma_out) free_stage();
       int v[2][32];
       tmem_get(src, v[0]);
 #pragma unroll
@@ -599,7 +661,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
         } else if (p.dtype == SSMQ_F32) {
           if (q == 2) {
             send_stage(t0);
-            free_stage();
+            if (one) tma_stores_read();
+            tc::named_sync(half_bar, 128);
           }
           stage_tokens<float>(c, xs[q], v[q & 1], at + ((q & 1) * 32 * kRows + col) * 4);
         } else if (p.dtype == SSMQ_F16) {
@@ -610,12 +673,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
       }
       if (p.tma_out) send_stage(p.dtype == SSMQ_F32 ? t0 + 64 : t0);
     }
-    if (quarter == 0 && lane == 0)  // the stores are done before the CTA leaves
+    for (; t < tiles; t += pairs) {  // after a wait gave up
+      int64_t ch, tok;
+      tile_at(p, t, ch, tok);
+      poison_tokens(p, channel_of(p, ch * kPairCh + rank * kRows + quarter * 32 + lane),
+                    tok * kPairTok + half, kPairTok / 2);
+    }
+    if (one)  // the stores are done before the CTA leaves
       asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncwarp();
   tc::fence_before();
   cluster_sync();  // the pair's MMAs, copies and remote arrivals are done
+  if (*gave_up) {  // (the same in both CTAs) or may still be in flight
+    if (warp == 0 && lane == 0 && rank == 0) {
+      // Both CTAs' copies count on the leader's barriers.  A stage that only one of
+      // them filled is made to expect that one's bytes; the last kPairStages uses are
+      // the only ones that can be open.
+      const int64_t theirs = *other_uses, most = uses > theirs ? uses : theirs;
+      for (int64_t j = most > kPairStages ? most - kPairStages : 0; j < most; ++j) {
+        uint64_t* bar = full + j % kPairStages;
+        if (j >= uses)
+          stream::expect_tx(bar, kPairStage);
+        else if (j >= theirs)
+          complete_tx(bar, kPairStage);
+        tc::mbar_wait(bar, (uint32_t)(j / kPairStages) & 1u, kWaitLimit);
+      }
+    }
+    if (warp == 1 && lane == 0) {
+      if (rank == 0) commit_pair(idle);
+      tc::mbar_wait(idle, 0, kWaitLimit);
+    }
+    __syncwarp();
+    cluster_sync();
+  }
   if (warp == 2)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
   if (threadIdx.x == 0 && *gave_up) flag_status(p.status, SSMQ_DEV_TIMEOUT);
@@ -789,6 +880,7 @@ cudaError_t launch_int8_linear(const ssmq_linear_args& a, void* ws, cudaStream_t
   p.ldy = a.y_stride;
   p.dtype = a.dtype;
   p.status = a.status;
+  p.wait_limit = stream::wait_limit();
   if (p.kblocks == 0) {
     const int64_t n = (p.M * p.N + 255) / 256, most = (int64_t)sm_count() * 8;
     bias_rows_kernel<<<(unsigned)(n < most ? n : most), 256, 0, st>>>(p);
