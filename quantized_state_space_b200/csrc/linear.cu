@@ -293,7 +293,8 @@ __device__ __forceinline__ void tma_stores_read() {
 // the memory's bandwidth, so the CTAs of a cluster take consecutive parts of K
 // of the same tile; each CTA then sums its share of the token columns from all
 // parts (32-bit integers pushed through distributed shared memory: exact, no
-// workspace, no second launch).
+// workspace, no second launch).  A wait that gives up raises a word in every CTA of the
+// cluster; they then write NaN to the tile and wait for copies and MMAs in flight.
 constexpr int kSplitThreads = 192;  // 4 epilogue warps, 1 TMA, 1 MMA
 constexpr int kMaxSplit = 4;  // (clusters of 8 such CTAs waited for SMs: 12 us against 8)
 
@@ -359,31 +360,33 @@ __global__ void __launch_bounds__(kSplitThreads)
   if (split > 1) cluster_sync();  // every CTA of the cluster runs before one pushes to it
   tc::fence_after();
   const uint32_t tmem = *slot;
+  auto give_up = [&] {  // (after the barrier above: the other CTAs' words are set up)
+    *gave_up = 1;
+    for (int r = 0; split > 1 && r < split; ++r)
+      store_remote(mapa(tc::smem_u32(slot + 1), (uint32_t)r), 1u);
+  };
 
+  int issued = 0;  // stages filled
   if (warp == 4 && lane == 0) {
     int s = 0;
     uint32_t phase = 0;
     int kb = kb0 + first;
     for (; kb < kb1; ++kb) {
-      if (!tc::mbar_wait(empty + s, phase, kWaitLimit)) {
-        *gave_up = 1;
+      if (!tc::mbar_wait(empty + s, phase, p.wait_limit)) {
+        give_up();
         break;
       }
       load(kb, s);
       if (++s == stages) s = 0, phase ^= 1u;
     }
-    if (*gave_up) {  // copies in flight land before the CTA leaves
-      const int n = kb - kb0;  // copies issued
-      for (int j = n > stages ? n - stages : 0; j < n; ++j)
-        tc::mbar_wait(full + j % stages, (uint32_t)(j / stages) & 1u, kWaitLimit);
-    }
+    issued = kb - kb0;
   } else if (warp == 5 && lane == 0) {
     constexpr uint32_t idesc = idesc_i8(kRows, kTok);
     int s = 0;
     uint32_t phase = 0;
     for (int kb = kb0; kb < kb1; ++kb) {
       if (!tc::mbar_wait(full + s, phase, kWaitLimit)) {
-        *gave_up = 1;
+        give_up();
         break;
       }
       tc::fence_after();
@@ -407,11 +410,11 @@ __global__ void __launch_bounds__(kSplitThreads)
   if (warp < 4) {
     c = channel_of(p, ch0 + ch);
     float xs = split == 1 ? token_scale(p, tok0, kLd) : 0.0f;
-    if (!tc::mbar_wait(done, 0, kWaitLimit)) *gave_up = 1;
-    __syncwarp();
+    const bool ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(done, 0, p.wait_limit));
+    if (!ok && lane == 0) give_up();
     tc::fence_after();
     for (int j = 0; j < kTok; j += kLd) {
-      if (tok0 + j >= p.M) break;
+      if (!ok || tok0 + j >= p.M) break;
       int v[kLd];
       tmem_get(lanes + j, v);
       tmem_done(v);
@@ -459,6 +462,14 @@ __global__ void __launch_bounds__(kSplitThreads)
   }
   tc::fence_before();
   __syncthreads();
+  if (*gave_up) {  // (raised in front of the barriers above)
+    if (warp == 4 && lane == 0)  // the last `stages` copies are the only ones still open
+      for (int j = issued > stages ? issued - stages : 0; j < issued; ++j)
+        tc::mbar_wait(full + j % stages, (uint32_t)(j / stages) & 1u, kWaitLimit);
+    if (warp == 5) tc::mbar_wait(done, 0, kWaitLimit);
+    if (warp < 4) poison_tokens(p, c, tok0 + (int64_t)rank * per, per);
+    __syncwarp();
+  }
   if (warp == 5) tc::tmem_dealloc(tmem, Cfg::kCols);
   if (threadIdx.x == 0 && *gave_up) flag_status(p.status, SSMQ_DEV_TIMEOUT);
 }

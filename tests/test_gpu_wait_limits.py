@@ -42,3 +42,13 @@ def linear_gives_up(monkeypatch, m, n, k, dtype, off):
 @pytest.mark.parametrize("m,n,k", [(4096, 2560, 512), (500, 500, 128), (5000, 5000, 1040)])
 def test_product_of_many_tokens(monkeypatch, m, n, k, dtype, off):
     linear_gives_up(monkeypatch, m, n, k, dtype, off)
+
+
+# token tiles of 16 to 128 columns, K whole or in 2 or 4 parts (the first four copies
+# or more need no wait: a short K gives up in the epilogue alone)
+@pytest.mark.parametrize("dtype,off", [(F16, 16), (BF16, 3), (F32, 16)])
+@pytest.mark.parametrize("m,n,k", [(1, 300, 640), (4, 1000, 4096), (64, 4096, 8192),
+                                   (90, 3000, 8192), (777, 1801, 1536), (300, 20000, 640),
+                                   (30, 5000, 3008), (20, 300, 16)])
+def test_product_of_few_tokens(monkeypatch, m, n, k, dtype, off):
+    linear_gives_up(monkeypatch, m, n, k, dtype, off)
