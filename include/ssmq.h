@@ -74,8 +74,9 @@ typedef enum {
                                  For tests of this path, the environment variable
                                  SSMQ_WAIT_LIMIT=<probes> (read at each call) lowers
                                  the limit of the waits for copies in
-                                 ssmq_quantize_groups and ssmq_int8_linear;
-                                 0 makes them give up at once. */
+                                 ssmq_quantize_groups and ssmq_int8_linear and of
+                                 the gated scan's waits; 0 makes them give up at
+                                 once. */
 
 typedef enum {
   SSMQ_F32 = 0,
@@ -819,7 +820,8 @@ ssmq_status ssmq_int8_linear(const ssmq_linear_args* args, void* workspace, size
  * ssmq_gated_update: one step in place on state (fp32 (b, d), dense); seqlen
  *   is 1 and only the batch strides count.  y may be exactly z.
  *
- * status: device word or NULL, SSMQ_DEV_TIMEOUT if a bounded device wait gave up.
+ * status: device word or NULL, SSMQ_DEV_TIMEOUT if a bounded device wait gave up;
+ * what such a call did not finish of its outputs is NaN.
  * The order of every sum depends on the sizes alone: a call repeated on the
  * same inputs on the same alignments gives the same bytes.  No workspace.
  * Errors: INVALID_ARG (NULL, negative sizes, bad strides, overlaps),

@@ -38,6 +38,7 @@ struct ScanParams {
   float* states;
   const int32_t* lengths;
   uint32_t* status;
+  uint32_t wait_limit;  // probes before a wait gives up
 };
 
 template <typename T, int kMode, int kLanes, bool kGate>
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T
     }
     const int buf = (int)(k % St::kBufs);
     if constexpr (kMode == kTma) {
-      if (threadIdx.x == 0) {
+      if (threadIdx.x == 0 && !flags) {
         const int c = (int)(blk * TileT::kChannels), t = (int)((k * size + rank) * TileT::kLen);
         stream::expect_tx(full + buf, kTensors * St::kTensorBytes);
 #pragma unroll
@@ -102,17 +103,17 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T
       St::commit();
     }
   };
+  carry_init(sh, size);
   if constexpr (kMode == kTma) {
     if (threadIdx.x == 0)
       for (int i = 0; i < St::kBufs; ++i) tc::mbar_init(full + i, 1);
     __syncthreads();
   }
-  carry_init(sh, size);
   for (int k = 0; k < kAhead; ++k) fetch(k);
   for (int64_t k = 0; k < rounds; ++k) {
     const int buf = (int)(k % St::kBufs);
     if constexpr (kMode == kTma) {
-      if (!tc::mbar_wait(full + buf, (uint32_t)(k / St::kBufs) & 1u, kWaitLimit))
+      if (!flags && !wait_tile(full + buf, (uint32_t)(k / St::kBufs) & 1u, p.wait_limit))
         flags |= SSMQ_DEV_TIMEOUT;
     } else {
       fetch(k + kAhead);
@@ -140,11 +141,11 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T
       a = fmul2(a, f[i]);
       b = ffma2(f[i], b, u[i]);
     }
-    float2 s = carry_in<TileT, false>(sh, k, make_float4(a.x, a.y, b.x, b.y), h, rank,
-                                       size, flags, [&] {
-                                         // (the tile before this one is read: its buffer is free)
-                                         if constexpr (kMode == kTma) fetch(k + kAhead);
-                                       });
+    float2 s = carry_in<TileT, false>(sh, k, make_float4(a.x, a.y, b.x, b.y), h, rank, size,
+                                      p.wait_limit, flags, [&] {
+                                        // (the tile before this one is read: its buffer is free)
+                                        if constexpr (kMode == kTma) fetch(k + kAhead);
+                                      });
     if (p.states && t0 < p.L && t0 % kGatedStateSteps == 0) {
       float* o = p.states + (seq * p.saved + t0 / kGatedStateSteps) * p.d + c0;
       if (in0) o[0] = s.x;
@@ -172,13 +173,18 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T
       }
     }
   }
+  if (kMode == kTma && flags && threadIdx.x == 0) {  // the copies in flight land
+    const int64_t k = sh.leave_at;
+    for (int64_t j = k; j < rounds && j < k + kAhead; ++j)
+      wait_tile(full + j % St::kBufs, (uint32_t)(j / St::kBufs) & 1u, kWaitLimit);
+  }
   if (p.h_final && rank == 0 && warp == 0 && sub == 0) {
     float* o = p.h_final + seq * p.d + c0;
     if (in0) o[0] = h.x;
     if (in1) o[next] = h.y;
   }
   flag_status(p.status, flags);
-  carry_done(size);
+  carry_done(sh, rounds, size, flags);
 }
 
 template <typename T>
@@ -201,6 +207,7 @@ cudaError_t scan_type(const ssmq_gated_args& a, cudaStream_t st) {
   p.states = a.states;
   p.lengths = a.lengths;
   p.status = a.status;
+  p.wait_limit = stream::wait_limit();
   const bool vec = a.dim % 2 == 0 && pairs_ok<T>(a.v) && pairs_ok<T>(a.g) && pairs_ok<T>(a.z) &&
                    pairs_ok<T>(a.y);
   const bool z = a.z.p != nullptr;

@@ -311,9 +311,17 @@ __device__ __forceinline__ void push_f4(float4* local, uint64_t* bar, uint32_t r
       : "memory");
 }
 
-// tc::mbar_wait, acquiring what the other CTAs of the cluster wrote
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+// Probes at most `limit` times; false means it gave up.
+__device__ __forceinline__ bool wait_tile(uint64_t* bar, uint32_t parity, uint32_t limit) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < limit; ++i)
+    if (tc::mbar_try(bar, parity)) return true;
+  return false;
+}
+// The same, acquiring what the other CTAs of the cluster wrote
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uint32_t limit) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < limit; ++i) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -342,17 +350,43 @@ __device__ __forceinline__ float4 shfl_f4(float4 v, int src) {
                      __shfl_sync(0xFFFFFFFFu, v.z, src), __shfl_sync(0xFFFFFFFFu, v.w, src));
 }
 
+// What this CTA expects on `bar` less `bytes` that will not come.
+__device__ __forceinline__ void complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(
+                   tc::smem_u32(bar)),
+               "r"(bytes)
+               : "memory");
+}
+// the same word of shared memory in CTA `rank` of the cluster
+__device__ __forceinline__ void store_remote(const uint32_t* local, uint32_t rank, uint32_t v) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::smem_u32(local)), "r"(rank));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ float2 nan2() {
+  return make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
+}
+
 template <typename TileT>
 struct Shared {
   static constexpr int kWarps = TileT::kWarps, kLanes = TileT::kLanes;
+  static constexpr int kMost = kLanes == 32 ? 8 : kMaxCluster;  // (wide blocks: portable clusters)
   float4 warp[2][kWarps][kLanes];
-  float4 cta[2][kLanes == 32 ? 8 : kMaxCluster][kLanes];  // (wide blocks: portable clusters)
+  float4 cta[2][kMost][kLanes];
   uint64_t bar[2];  // the maps of all CTAs of a round have arrived
+  // After a wait gave up: the round at whose barrier the CTA left the exchange (kNever:
+  // it has not), whether any CTA of the cluster gave up, the rounds that each has pushed.
+  uint32_t leave_at, left, pushed[kMost];
 };
+constexpr uint32_t kNever = 0xFFFFFFFFu;
 
-// Before the first round (every thread of the cluster).
+// Before the first round (every thread of the cluster).  All threads write the words:
+// a branch for one of them here cost the gradient's word form 100 bytes of spills (307
+// us against 271 at 8 x 2048 x 1537 binary16).
 template <typename TileT>
 __device__ __forceinline__ void carry_init(Shared<TileT>& sh, uint32_t size) {
+  sh.leave_at = kNever;
+  sh.left = 0;
   if (size == 1) return;
   if (threadIdx.x == 0) {
     tc::mbar_init(sh.bar, 1);
@@ -360,10 +394,58 @@ __device__ __forceinline__ void carry_init(Shared<TileT>& sh, uint32_t size) {
   }
   cluster_sync();
 }
-// Behind the last one: nobody pushes to a CTA that has left.
-__device__ __forceinline__ void carry_done(uint32_t size) {
+// A thread whose wait gives up raises its flags.  At the CTA's next barrier all its
+// threads learn of it (flags != 0 in every one) and leave the exchange: they wait for
+// nothing, fetch and push nothing, and go through the rounds with a NaN state, so that
+// what the CTA has not finished is NaN.  Returns that state.
+template <typename TileT>
+__device__ __forceinline__ float2 leave(Shared<TileT>& sh, int64_t k) {
+  if (threadIdx.x == 0 && sh.leave_at == kNever) sh.leave_at = (uint32_t)k;
+  return nan2();
+}
+// Behind the last round: nobody pushes to a CTA that has left.  A CTA that gave up has
+// pushed k rounds only, so barriers may be open: the one that this CTA has armed for
+// round k - 1, less what was never sent, and the one of round k, not armed yet, to which
+// the others may have pushed.  (Round k - 2 had arrived before this CTA pushed round
+// k - 1, and nobody pushes round k + 1 without this CTA's round k.)
+template <typename TileT>
+__device__ __forceinline__ void carry_done(Shared<TileT>& sh, int64_t rounds, uint32_t size,
+                                           uint32_t flags) {
+  if (size == 1) return;
+  if (flags) {
+    for (uint32_t r = 0; r < size; ++r) store_remote(&sh.left, r, 1u);
+    // (cluster_meet orders nothing by itself)
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  }
   __syncwarp();
-  if (size > 1) cluster_meet();
+  cluster_meet();
+  if (*const_cast<volatile uint32_t*>(&sh.left) == 0) return;
+  // (the same in every CTA of the cluster)
+  if (threadIdx.x == 0) {
+    const uint32_t k = sh.leave_at != kNever ? sh.leave_at : (uint32_t)rounds;
+    for (uint32_t r = 0; r < size; ++r) store_remote(sh.pushed + cluster_rank(), r, k);
+  }
+  __syncwarp();
+  cluster_sync();
+  if (threadIdx.x == 0) {
+    constexpr uint32_t kBytes = TileT::kLanes * (uint32_t)sizeof(float4);
+    const uint32_t k = sh.pushed[cluster_rank()];
+    uint32_t last = 0, now = 0;  // CTAs that pushed round k - 1, round k
+    for (uint32_t r = 0; r < size; ++r) {
+      last += sh.pushed[r] >= k;
+      now += sh.pushed[r] > k;
+    }
+    if (k > 0) {
+      uint64_t* bar = sh.bar + ((k - 1) & 1u);
+      if (last < size) complete_tx(bar, (size - last) * kBytes);
+      wait_tile(bar, ((k - 1) >> 1) & 1u, kWaitLimit);
+    }
+    if (now > 0) {
+      uint64_t* bar = sh.bar + (k & 1u);
+      stream::expect_tx(bar, now * kBytes);
+      wait_tile(bar, (k >> 1) & 1u, kWaitLimit);
+    }
+  }
 }
 
 // State entering this thread's segment, from the segments' maps in step order
@@ -373,11 +455,12 @@ __device__ __forceinline__ void carry_done(uint32_t size) {
 // pushes round k + 2 only after it has every map of round k + 1, and a CTA pushes
 // round k + 1 only when its threads are done with round k.  met() runs behind the
 // CTA's barrier: every thread is done with the rounds before this one, and with
-// what it read of this round before the call.
+// what it read of this round before the call.  kReverse: flags are the CTA's already
+// (a barrier lies between the round's waits and the call).
 template <typename TileT, bool kReverse, typename Met>
 __device__ __forceinline__ float2 carry_in(Shared<TileT>& sh, int64_t k, float4 m, float2& h,
-                                           uint32_t rank, uint32_t size, uint32_t& flags,
-                                           Met met) {
+                                           uint32_t rank, uint32_t size, uint32_t limit,
+                                           uint32_t& flags, Met met) {
   const int buf = (int)(k & 1);
   constexpr int kSubs = TileT::kSubs, kLanes = TileT::kLanes, kWarps = TileT::kWarps;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -398,7 +481,11 @@ __device__ __forceinline__ float2 carry_in(Shared<TileT>& sh, int64_t k, float4 
     const float4 before = shfl_f4(m, src & 31);
     if (sub > 0) mine = before;
   }
-  __syncthreads();
+  if constexpr (kReverse)
+    __syncthreads();
+  else
+    flags = __syncthreads_or(flags) ? SSMQ_DEV_TIMEOUT : 0;
+  if (flags) h = leave(sh, k);
   met();
   float4 pre = make_float4(1.0f, 1.0f, 0.0f, 0.0f), all = pre;
 #pragma unroll
@@ -409,15 +496,18 @@ __device__ __forceinline__ float2 carry_in(Shared<TileT>& sh, int64_t k, float4 
   float2 base = h;
   if (size > 1) {
     // warp i tells CTA i (and i + 8) of the cluster what this CTA's tile does to a state
-    if (threadIdx.x == 0)
+    const uint32_t live = flags ? 0 : size;
+    if (threadIdx.x == 0 && !flags)
       stream::expect_tx(sh.bar + buf, size * kLanes * (uint32_t)sizeof(float4));
     if (sub0 == 0)
-      for (uint32_t r = (uint32_t)warp; r < size; r += kWarps)
+      for (uint32_t r = (uint32_t)warp; r < live; r += kWarps)
         push_f4(&sh.cta[buf][rank][l], sh.bar + buf, r, all);
-    if (!wait_cluster(sh.bar + buf, (uint32_t)(k >> 1) & 1u))
-      flags |= SSMQ_DEV_TIMEOUT;
-    __syncwarp();
     float2 s = h;
+    if (!wait_cluster(sh.bar + buf, (uint32_t)(k >> 1) & 1u, flags ? 0 : limit)) {
+      flags |= SSMQ_DEV_TIMEOUT;
+      s = base = nan2();
+    }
+    __syncwarp();
     // (four loads at a time, which do not wait on one another; size is 2, 4, 8 or 16,
     // and the entries of a cluster of 2 end after two)
     for (uint32_t r = 0; r < size; r += 4) {

@@ -35,6 +35,7 @@ struct GradParams {
   float* dh0;
   const int32_t* lengths;
   uint32_t* status;
+  uint32_t wait_limit;  // probes before a wait gives up
 };
 
 template <typename T, int kMode, int kLanes, bool kGate>
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kGradCtas)
     const int64_t tile = tile_of(k);
     const int buf = (int)(k % St::kBufs);
     if constexpr (kMode == kTma) {
-      if (threadIdx.x == 0 && k < rounds && tile >= 0) {
+      if (threadIdx.x == 0 && !flags && k < rounds && tile >= 0) {
         const int c = (int)(blk * TileT::kChannels), t = (int)(tile * TileT::kLen);
         stream::expect_tx(full + buf, (kGate ? 4 : 3) * St::kTensorBytes);
 #pragma unroll
@@ -111,12 +112,12 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kGradCtas)
       St::commit();
     }
   };
+  carry_init(sh, size);
   if constexpr (kMode == kTma) {
     if (threadIdx.x == 0)
       for (int i = 0; i < St::kBufs; ++i) tc::mbar_init(full + i, 1);
     __syncthreads();
   }
-  carry_init(sh, size);
   for (int k = 0; k < St::kBufs; ++k) fetch(k);
   for (int64_t k = 0; k < rounds; ++k) {
     const int buf = (int)(k % St::kBufs);
@@ -131,7 +132,8 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kGradCtas)
       hs = make_float2(sp[0], sp[next]);
     }
     if constexpr (kMode == kTma) {
-      if (real && !tc::mbar_wait(full + buf, (uint32_t)(k / St::kBufs) & 1u, kWaitLimit))
+      if (real && !flags &&
+          !wait_tile(full + buf, (uint32_t)(k / St::kBufs) & 1u, p.wait_limit))
         flags |= SSMQ_DEV_TIMEOUT;
       if (left < kSteps) stage.clear(buf, left);
     } else {
@@ -172,7 +174,8 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kGradCtas)
         const float4 before = shfl_f4(m, (lane - kLanes) & 31);
         if (sub > 0) mine = before;
       }
-      __syncthreads();
+      flags = __syncthreads_or(flags) ? SSMQ_DEV_TIMEOUT : 0;
+      if (flags) hs = nan2();  // (dz goes out next)
 #pragma unroll
       for (int w = 0; w < TileT::kWarps - 1; ++w) {
         const float4 e = s_fwd[k & 1][w][l];
@@ -210,9 +213,10 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kGradCtas)
     float2 r = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = kSteps - 1; i >= 0; --i) r = fmul2(f[i], fadd2(dh[i], r));
-    r = carry_in<TileT, true>(sh, k, make_float4(a.x, a.y, r.x, r.y), c, rank, size, flags, [&] {
-      fetch(k + St::kBufs);  // (every thread has read this round's tile)
-    });
+    r = carry_in<TileT, true>(sh, k, make_float4(a.x, a.y, r.x, r.y), c, rank, size,
+                              p.wait_limit, flags, [&] {
+                                fetch(k + St::kBufs);  // (every thread has read this tile)
+                              });
     T* dvo = dvp + (t0 + kSteps - 1) * p.dv.rs;
     T* dgo = dgp + (t0 + kSteps - 1) * p.dg.rs;
     // gradients of step i, from the last step backwards
@@ -237,13 +241,18 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kGradCtas)
       for (int i = kSteps - 1; i >= 0; --i) put(i, i < left, t0 + i < p.L);
     }
   }
+  if (kMode == kTma && flags && threadIdx.x == 0) {  // the copies in flight land
+    const int64_t k = sh.leave_at;
+    for (int64_t j = k; j < rounds && j < k + St::kBufs && tile_of(j) >= 0; ++j)
+      wait_tile(full + j % St::kBufs, (uint32_t)(j / St::kBufs) & 1u, kWaitLimit);
+  }
   if (p.dh0 && rank == 0 && warp == 0 && sub == 0) {
     float* o = p.dh0 + seq * p.d + c0;
     if (in0) o[0] = c.x;
     if (in1) o[next] = c.y;
   }
   flag_status(p.status, flags);
-  carry_done(size);
+  carry_done(sh, rounds, size, flags);
 }
 
 template <typename T>
@@ -269,6 +278,7 @@ cudaError_t grad_type(const ssmq_gated_grad_args& a, cudaStream_t st) {
   p.dh0 = a.dh0;
   p.lengths = a.lengths;
   p.status = a.status;
+  p.wait_limit = stream::wait_limit();
   const bool z = a.z.p != nullptr;
   const bool vec = a.dim % 2 == 0 && pairs_ok<T>(a.v) && pairs_ok<T>(a.g) && pairs_ok<T>(a.dy) &&
                    pairs_ok<T>(a.dv) && pairs_ok<T>(a.dg) &&

@@ -52,3 +52,75 @@ def test_product_of_many_tokens(monkeypatch, m, n, k, dtype, off):
                                    (30, 5000, 3008), (20, 300, 16)])
 def test_product_of_few_tokens(monkeypatch, m, n, k, dtype, off):
     linear_gives_up(monkeypatch, m, n, k, dtype, off)
+
+
+def padded(gen, b, L, d, pad, dtype):
+    """(b, L, d) in rows of d + pad elements, with one more sequence behind."""
+    wide = torch.randn(b + 1, L, d + pad, generator=gen).to(dtype).to(dev())
+    return wide[:b, :, :d]
+
+
+def guarded(b, L, d, pad, dtype):
+    """The same layout to write to, and all of it: 7 where nothing was written."""
+    wide = torch.full((b + 1, L, d + pad), 7.0, dtype=dtype, device=dev())
+    return wide[:b, :, :d], wide
+
+
+def untouched(wide, b, d):
+    return (wide[b:] == 7).all() and (wide[:, :, d:] == 7).all()
+
+
+def all_nan(*ts):
+    return all(bool(torch.isnan(t).all()) for t in ts)
+
+
+# rows on 16 bytes (copies by TMA), even rows (pairs), odd rows (single channels, and
+# words in the gradient); one round and many, whole clusters and a single CTA
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("pad", [0, 2, 3])
+@pytest.mark.parametrize("z", [False, True])
+@pytest.mark.parametrize("b,L,d", [(2, 300, 64), (1, 9000, 48), (64, 70, 2560), (3, 40, 40)])
+def test_gated_recurrence(monkeypatch, b, L, d, z, pad, dtype):
+    gen = torch.Generator().manual_seed(L + d)
+    v, g, dy = (padded(gen, b, L, d, pad, dtype) for _ in range(3))
+    zz = padded(gen, b, L, d, pad, dtype) if z else None
+    h0, dh = (torch.randn(b, d, generator=gen).to(dev()) for _ in range(2))
+    st = status_word()
+    # (a sequence of one tile in a CTA that copies for itself waits for nothing)
+    waits = pad == 0 or L > 256 or (L > 64 and b * d < 10000)
+    fwd = lambda y: api.gated_scan(v, g, z=zz, h0=h0, y=y, save_states=True, status=st)
+    bwd = lambda s, dv, dg, dz: api.gated_scan_backward(dy, v, g, s, z=zz, dh_final=dh, dv=dv,
+                                                        dg=dg, dz=dz, status=st)
+    outs = [guarded(b, L, d, pad, dtype) for _ in range(4 if z else 3)]
+    y, wides = outs[0][0], [o[1] for o in outs]
+    grads = [o[0] for o in outs[1:]] + ([] if z else [None])
+    _, h, states = fwd(y)
+    ref = [t.clone() for t in (y, h, states)]
+    ref_g = [t.clone() for t in bwd(states, *grads) if t is not None]
+    assert int(st) == 0
+
+    for w in wides:
+        w.fill_(7)
+    monkeypatch.setenv("SSMQ_WAIT_LIMIT", "0")
+    _, h, s = fwd(y)
+    torch.cuda.synchronize()
+    assert int(st) == (N.DEV_TIMEOUT if waits else 0)
+    if waits:
+        assert all_nan(y, h, s)
+    st.zero_()
+    dv, dg, dz, dh0 = bwd(ref[2], *grads)
+    torch.cuda.synchronize()
+    assert int(st) == (N.DEV_TIMEOUT if waits else 0)
+    if waits:
+        assert all_nan(dv, dg, dh0)
+        if z and pad == 0:  # (else the first round's are whole: they need no exchange)
+            assert all_nan(dz)
+    assert all(untouched(w, b, d) for w in wides)
+
+    monkeypatch.delenv("SSMQ_WAIT_LIMIT")
+    st.zero_()
+    again = [t for t in fwd(y)]
+    again_g = [t for t in bwd(again[2], *grads) if t is not None]
+    assert int(st) == 0
+    for r, t in zip(ref + ref_g, again + again_g):
+        assert torch.equal(r, t)
