@@ -636,6 +636,16 @@ def _call(device, entry, *fields):
             entry(torch._C._cuda_getCurrentRawStream(i), *fields)
 
 
+def _no_gradient(call, *tensors):
+    """The call defines no gradient: inputs (and outputs it is to write) that
+    require one are refused, not returned without it."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError("%s defines no gradient: detach the tensors that require one, or "
+                                 "call it under torch.no_grad()" % call)
+
+
 def _cuda(t, name, dim=None):
     """The device and type id of a call's leading tensor."""
     if not t.is_cuda:
@@ -705,7 +715,9 @@ def rms_norm_quantize(x, weight=None, *, residual=None, eps=1e-5, residual_out=N
     values (in x's dtype) when want_y.  codes (..., d) int8 and scales (...)
     float32 feed int8_linear.  residual_out may be x or residual itself (in
     place).  want_codes=False leaves the codes out (codes and scales are then
-    None).  Codes that the call allocates lie on 16-byte rows."""
+    None).  Codes that the call allocates lie on 16-byte rows.  There is no
+    gradient: tensors that require one are refused."""
+    _no_gradient("rms_norm_quantize", x, weight, residual, residual_out, scales, y)
     dv, kind = _cuda(x, "x")
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x must have at least one channel")
@@ -761,7 +773,9 @@ def int8_linear(x, x_scale, w, w_scale, *, bias=None, out=None, dtype=None, work
     (float16 by default, bfloat16 or float32) or in out's.  Rows of x and w on
     16-byte boundaries (such as the codes of rms_norm_quantize) are read in
     place; others are first copied into ``workspace`` (uint8 bytes on the
-    device, allocated when not given)."""
+    device, allocated when not given).  There is no gradient: scales and bias
+    that require one are refused."""
+    _no_gradient("int8_linear", x_scale, w_scale, bias, out)
     if out is not None:
         if dtype is not None and dtype != out.dtype:
             raise ValueError("dtype %s differs from out's %s" % (dtype, out.dtype))
@@ -896,6 +910,7 @@ def gated_scan(v, g, *, z=None, h0=None, lengths=None, y=None, h_final=None, sta
                              "requires_grad")
         out, h = _GatedScan.apply(v, g, z, h0, lengths)
         return out, (h if return_state else None)
+    _no_gradient("gated_scan on its caller's outputs", y, h_final, states)
     y, h_final, states = _gated_scan(v, g, z, h0, lengths, y, h_final, states, return_state,
                                      save_states, status)
     return (y, h_final, states) if states is not None else (y, h_final)
@@ -906,7 +921,8 @@ def gated_scan_backward(dy, v, g, states, *, z=None, dh_final=None, lengths=None
     """Gradients (dv, dg, dz, dh0) of a gated_scan call with save_states: dy
     (b, L, d) and dh_final (b, d) float32 or None are the gradients of its
     outputs; dz is None without z.  Outputs may be given; dv, dg and dz may be
-    exactly v, g, z or dy (each a different one)."""
+    exactly v, g, z or dy (each a different one).  The results are values: no
+    second derivative is recorded, whatever the inputs require."""
     dev, kind = _cuda(v, "v", 3)
     shape, dt = v.shape, v.dtype
     b, L, d = shape
@@ -948,7 +964,9 @@ def gated_scan_backward(dy, v, g, states, *, z=None, dh_final=None, lengths=None
 def gated_update(state, v, g, *, z=None, y=None):
     """One step of the gated recurrence in place on ``state`` (b, d) float32;
     v, g, z (b, d) with contiguous channels.  Returns y (b, d) in v's dtype
-    (y may be z itself)."""
+    (y may be z itself).  There is no gradient (gated_scan has one): tensors
+    that require one are refused."""
+    _no_gradient("gated_update", state, v, g, z, y)
     dv, kind = _cuda(v, "v", 2)
     shape, dt = v.shape, v.dtype
     b, d = shape

@@ -1,0 +1,43 @@
+"""Autograd and the quantized-layer operators: a derivative is computed or refused,
+never dropped.  The refusals come before anything else, so most need no GPU."""
+import pytest
+import torch
+
+from quantized_state_space_b200 import api
+
+
+def f32(*shape, grad=False):
+    return torch.ones(*shape, requires_grad=grad)
+
+
+CALLS = {
+    "rms_norm_quantize": (lambda t: api.rms_norm_quantize(
+        t["x"], t["weight"], residual=t["residual"], residual_out=t["residual_out"], y=t["y"]),
+        dict(x=(4, 16), weight=(16,), residual=(4, 16), residual_out=(4, 16), y=(4, 16))),
+    "int8_linear": (lambda t: api.int8_linear(
+        torch.zeros(4, 16, dtype=torch.int8), t["x_scale"], torch.zeros(8, 16, dtype=torch.int8),
+        t["w_scale"], bias=t["bias"], out=t["out"]),
+        dict(x_scale=(4,), w_scale=(8,), bias=(8,), out=(4, 8))),
+    "gated_update": (lambda t: api.gated_update(t["state"], t["v"], t["g"], z=t["z"], y=t["y"]),
+                     dict(state=(4, 16), v=(4, 16), g=(4, 16), z=(4, 16), y=(4, 16))),
+}
+
+
+@pytest.mark.parametrize("call,name", [(c, n) for c, (_, s) in CALLS.items() for n in s])
+def test_gradients_are_refused(call, name):
+    fn, shapes = CALLS[call]
+    t = {n: f32(*s, grad=n == name) for n, s in shapes.items()}
+    with pytest.raises(ValueError, match="%s defines no gradient" % call):
+        fn(t)
+    # without gradients, and under no_grad, the call goes on (to refuse CPU tensors)
+    with pytest.raises(ValueError, match="CUDA|cuda"):
+        fn({n: f32(*s) for n, s in shapes.items()})
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA|cuda"):
+        fn(t)
+
+
+@pytest.mark.parametrize("name", ["y", "h_final", "states"])
+def test_scan_outputs_that_require_a_gradient(name):
+    v = f32(1, 4, 16)
+    with pytest.raises(ValueError, match="defines no gradient"):
+        api.gated_scan(v, v, **{name: f32(1, 4, 16, grad=True)})
