@@ -9,6 +9,7 @@ import contextlib
 import math
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _native as N
 
@@ -636,9 +637,19 @@ def _call(device, entry, *fields):
             entry(torch._C._cuda_getCurrentRawStream(i), *fields)
 
 
+def _no_tangent(call, *tensors):
+    """No call carries forward-mode derivatives: dual tensors are refused, not
+    returned without their tangents."""
+    if forward_ad._current_level >= 0:  # (inside forward_ad.dual_level)
+        for t in tensors:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError("%s defines no forward-mode derivative" % call)
+
+
 def _no_gradient(call, *tensors):
     """The call defines no gradient: inputs (and outputs it is to write) that
     require one are refused, not returned without it."""
+    _no_tangent(call, *tensors)
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
@@ -901,6 +912,7 @@ def gated_scan(v, g, *, z=None, h0=None, lengths=None, y=None, h_final=None, sta
     input requires a gradient, the result is differentiable; the caller's
     output tensors are then not accepted.  (To capture a training step in a
     CUDA graph, call gated_scan with save_states and gated_scan_backward.)"""
+    _no_tangent("gated_scan", v, g, z, h0)
     if torch.is_grad_enabled() and (v.requires_grad or g.requires_grad or
                                     (z is not None and z.requires_grad) or
                                     (h0 is not None and h0.requires_grad)):
@@ -923,6 +935,7 @@ def gated_scan_backward(dy, v, g, states, *, z=None, dh_final=None, lengths=None
     outputs; dz is None without z.  Outputs may be given; dv, dg and dz may be
     exactly v, g, z or dy (each a different one).  The results are values: no
     second derivative is recorded, whatever the inputs require."""
+    _no_tangent("gated_scan_backward", dy, v, g, states, z, dh_final)
     dev, kind = _cuda(v, "v", 3)
     shape, dt = v.shape, v.dtype
     b, L, d = shape

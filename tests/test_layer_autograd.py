@@ -2,6 +2,7 @@
 never dropped.  The refusals come before anything else, so most need no GPU."""
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 from quantized_state_space_b200 import api
 
@@ -41,3 +42,38 @@ def test_scan_outputs_that_require_a_gradient(name):
     v = f32(1, 4, 16)
     with pytest.raises(ValueError, match="defines no gradient"):
         api.gated_scan(v, v, **{name: f32(1, 4, 16, grad=True)})
+
+
+@pytest.mark.parametrize("call,name", [(c, n) for c, (_, s) in CALLS.items() for n in s])
+def test_tangents_are_refused(call, name):
+    fn, shapes = CALLS[call]
+    with forward_ad.dual_level():
+        t = {n: f32(*s) for n, s in shapes.items()}
+        t[name] = forward_ad.make_dual(t[name], torch.ones_like(t[name]))
+        for grad in (True, False):
+            with torch.set_grad_enabled(grad), \
+                    pytest.raises(ValueError, match="%s defines no forward-mode" % call):
+                fn(t)
+
+
+@pytest.mark.parametrize("name", ["v", "g", "z", "h0"])
+def test_scan_tangents_are_refused(name):
+    """For inputs that require a gradient as well."""
+    for grad in (False, True):
+        with forward_ad.dual_level():
+            t = {n: f32(1, 4, 16, grad=grad) for n in ("v", "g", "z")}
+            t["h0"] = f32(1, 16)
+            t[name] = forward_ad.make_dual(t[name], torch.ones_like(t[name]))
+            with pytest.raises(ValueError, match="gated_scan defines no forward-mode"):
+                api.gated_scan(t["v"], t["g"], z=t["z"], h0=t["h0"])
+
+
+@pytest.mark.parametrize("name", ["dy", "v", "g", "states", "z", "dh_final"])
+def test_scan_backward_tangents_are_refused(name):
+    with forward_ad.dual_level():
+        t = {n: f32(1, 4, 16) for n in ("dy", "v", "g", "z")}
+        t.update(states=f32(1, 1, 16), dh_final=f32(1, 16))
+        t[name] = forward_ad.make_dual(t[name], torch.ones_like(t[name]))
+        with pytest.raises(ValueError, match="gated_scan_backward defines no forward-mode"):
+            api.gated_scan_backward(t["dy"], t["v"], t["g"], t["states"], z=t["z"],
+                                    dh_final=t["dh_final"])
