@@ -10,6 +10,7 @@ import math
 
 import torch
 from torch.autograd import forward_ad
+from torch.autograd.graph import increment_version
 
 from . import _native as N
 
@@ -640,21 +641,30 @@ def _call(device, entry, *fields):
 def _no_tangent(call, *tensors):
     """No call carries forward-mode derivatives: dual tensors are refused, not
     returned without their tangents."""
-    if forward_ad._current_level >= 0:  # (inside forward_ad.dual_level)
-        for t in tensors:
-            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
-                raise ValueError("%s defines no forward-mode derivative" % call)
+    for t in tensors:
+        if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError("%s defines no forward-mode derivative" % call)
 
 
 def _no_gradient(call, *tensors):
     """The call defines no gradient: inputs (and outputs it is to write) that
     require one are refused, not returned without it."""
-    _no_tangent(call, *tensors)
+    if forward_ad._current_level >= 0:  # (inside forward_ad.dual_level)
+        _no_tangent(call, *tensors)
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
                 raise ValueError("%s defines no gradient: detach the tensors that require one, or "
                                  "call it under torch.no_grad()" % call)
+
+
+def _written(*tensors):
+    """The call has written these tensors of its caller (None: it made its own):
+    autograd's version of each counts on, so that a backward pass that saved one
+    of them raises instead of using the new contents."""
+    given = [t for t in tensors if t is not None]
+    if given:
+        increment_version(given)
 
 
 def _cuda(t, name, dim=None):
@@ -732,6 +742,7 @@ def rms_norm_quantize(x, weight=None, *, residual=None, eps=1e-5, residual_out=N
     dv, kind = _cuda(x, "x")
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x must have at least one channel")
+    given = residual_out, y, codes, scales
     shape, dt = x.shape, x.dtype
     d = shape[-1]
     tokens = x.numel() // d
@@ -773,6 +784,7 @@ def rms_norm_quantize(x, weight=None, *, residual=None, eps=1e-5, residual_out=N
         sp = scales.data_ptr()
     _call(dv, N.ssmq_rms_norm_quantize, tokens, d, kind, eps, xp, xs, rp, rs, wp, op, os, yp, ys,
           qp, qs, sp, 0 if status is None else _status_ptr(status, dv))
+    _written(*given)
     return (codes, scales) + out
 
 
@@ -808,6 +820,7 @@ def int8_linear(x, x_scale, w, w_scale, *, bias=None, out=None, dtype=None, work
     xsp = _dense(x_scale, "x_scale", torch.float32, tokens, dv)
     wsp = _dense(w_scale, "w_scale", torch.float32, n, dv)
     bp = 0 if bias is None else _dense(bias, "bias", torch.float32, n, dv)
+    given = out
     if out is None:
         out = torch.empty(*lead, n, dtype=dtype, device=dv)
         yp, yst = out.data_ptr(), n
@@ -824,6 +837,7 @@ def int8_linear(x, x_scale, w, w_scale, *, bias=None, out=None, dtype=None, work
                 workspace = torch.empty(ws + 256, dtype=torch.uint8, device=dv)
             wptr = (workspace.data_ptr() + 255) // 256 * 256
     _call(dv, N.ssmq_int8_linear, wptr, ws, *f)
+    _written(given)
     return out
 
 
@@ -851,6 +865,7 @@ def _saved_states(L):
 def _gated_scan(v, g, z, h0, lengths, y, h_final, states, return_state, save_states,
                 status=None):
     dv, kind = _cuda(v, "v", 3)
+    given = y, h_final, states
     shape, dt = v.shape, v.dtype
     b, L, d = shape
     if y is None:
@@ -875,6 +890,7 @@ def _gated_scan(v, g, z, h0, lengths, y, h_final, states, return_state, save_sta
           0 if h0 is None else _dense(h0, "h0", torch.float32, b * d, dv), hp, sp,
           0 if lengths is None else _dense(lengths, "lengths", torch.int32, b, dv),
           0 if status is None else _status_ptr(status, dv))
+    _written(*given)
     return y, h_final, states
 
 
@@ -912,7 +928,8 @@ def gated_scan(v, g, *, z=None, h0=None, lengths=None, y=None, h_final=None, sta
     input requires a gradient, the result is differentiable; the caller's
     output tensors are then not accepted.  (To capture a training step in a
     CUDA graph, call gated_scan with save_states and gated_scan_backward.)"""
-    _no_tangent("gated_scan", v, g, z, h0)
+    if forward_ad._current_level >= 0:
+        _no_tangent("gated_scan", v, g, z, h0)
     if torch.is_grad_enabled() and (v.requires_grad or g.requires_grad or
                                     (z is not None and z.requires_grad) or
                                     (h0 is not None and h0.requires_grad)):
@@ -935,8 +952,10 @@ def gated_scan_backward(dy, v, g, states, *, z=None, dh_final=None, lengths=None
     outputs; dz is None without z.  Outputs may be given; dv, dg and dz may be
     exactly v, g, z or dy (each a different one).  The results are values: no
     second derivative is recorded, whatever the inputs require."""
-    _no_tangent("gated_scan_backward", dy, v, g, states, z, dh_final)
+    if forward_ad._current_level >= 0:
+        _no_tangent("gated_scan_backward", dy, v, g, states, z, dh_final)
     dev, kind = _cuda(v, "v", 3)
+    given = dv, dg, dz, dh0
     shape, dt = v.shape, v.dtype
     b, L, d = shape
     if z is None and dz is not None:
@@ -971,6 +990,7 @@ def gated_scan_backward(dy, v, g, states, *, z=None, dh_final=None, lengths=None
           0 if dh_final is None else _dense(dh_final, "dh_final", torch.float32, b * d, dev), dp,
           0 if lengths is None else _dense(lengths, "lengths", torch.int32, b, dev),
           0 if status is None else _status_ptr(status, dev))
+    _written(*given)
     return dv, dg, dz, dh0
 
 
@@ -986,6 +1006,7 @@ def gated_update(state, v, g, *, z=None, y=None):
     if state is None:
         raise ValueError("state is required")
     hp = _dense(state, "state", torch.float32, b * d, dv)
+    given = y
     rows = []
     for t, name in ((v, "v"), (g, "g"), (z, "z"), (y, "y")):
         if t is not None:
@@ -999,4 +1020,5 @@ def gated_update(state, v, g, *, z=None, y=None):
         else:
             rows += _NONE
     _call(dv, N.ssmq_gated_update, b, 1, d, kind, *rows, 0, hp, 0, 0, 0)
+    _written(state, given)
     return y

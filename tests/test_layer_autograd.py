@@ -77,3 +77,50 @@ def test_scan_backward_tangents_are_refused(name):
         with pytest.raises(ValueError, match="gated_scan_backward defines no forward-mode"):
             api.gated_scan_backward(t["dy"], t["v"], t["g"], t["states"], z=t["z"],
                                     dh_final=t["dh_final"])
+
+
+def writers():
+    """(name, call, the tensors of the caller that it writes)"""
+    from gpu_util import dev
+    h = lambda *s: torch.ones(*s, device=dev())
+    x, g, z, state, q, r = h(4, 16), h(4, 16), h(4, 16), h(4, 16), h(4, 16), h(4, 16)
+    codes = torch.zeros(4, 16, dtype=torch.int8, device=dev())
+    seq, zs, h0 = h(2, 8, 16), h(2, 8, 16), h(2, 16)
+    st = api.gated_scan(seq, seq, save_states=True)[2]
+    grads = [h(2, 8, 16) for _ in range(3)] + [h(2, 16)]
+    sc, out = h(4), h(4, 4)
+    return [
+        ("residual in place", lambda: api.rms_norm_quantize(x, residual=r, residual_out=x), [x]),
+        ("norm", lambda: api.rms_norm_quantize(r, y=q, codes=codes, scales=sc), [q, codes, sc]),
+        ("product", lambda: api.int8_linear(codes, h(4), codes, h(4), out=out), [out]),
+        ("scan on z", lambda: api.gated_scan(seq, seq, z=zs, y=zs, h0=h0, h_final=h0, states=st),
+         [zs, h0, st]),
+        ("gradient", lambda: api.gated_scan_backward(seq, seq, seq, st, z=h(2, 8, 16),
+                                                     dv=grads[0], dg=grads[1], dz=grads[2],
+                                                     dh0=grads[3]), grads),
+        ("update on z", lambda: api.gated_update(state, x, g, z=z, y=z), [state, z]),
+    ]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("i", range(6))
+def test_written_tensors_count_on(i):
+    """A tensor that autograd saved and a call has written since is noticed."""
+    from gpu_util import dev
+    name, call, written = writers()[i]
+    before = [t._version for t in written]
+    w = [torch.ones(1, device=dev(), requires_grad=True) for _ in written]
+    losses = [(a * t).sum() for a, t in zip(w, written) if t.is_floating_point()]
+    call()
+    for t, v in zip(written, before):
+        assert t._version > v, name
+    for loss in losses:
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+
+
+@pytest.mark.gpu
+def test_written_tensors_of_inference_mode():
+    with torch.inference_mode():
+        for _, call, _ in writers():
+            call()
