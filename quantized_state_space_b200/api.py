@@ -901,6 +901,7 @@ class _GatedScan(torch.autograd.Function):
     def forward(ctx, v, g, z, h0, lengths):
         y, h_final, states = _gated_scan(v, g, z, h0, lengths, None, None, None, True, True)
         ctx.save_for_backward(v, g, z, lengths, states)
+        ctx.h0_shape = None if h0 is None else h0.shape  # (any of b d elements)
         return y, h_final
 
     @staticmethod
@@ -911,7 +912,7 @@ class _GatedScan(torch.autograd.Function):
             dy = dy.contiguous()  # (an expanded gradient, as of a sum)
         dv, dg, dz, dh0 = gated_scan_backward(dy, v, g, states, z=z,
                                               dh_final=dh_final.contiguous(), lengths=lengths)
-        return dv, dg, dz, dh0 if ctx.needs_input_grad[3] else None, None
+        return dv, dg, dz, dh0.view(ctx.h0_shape) if ctx.needs_input_grad[3] else None, None
 
 
 def gated_scan(v, g, *, z=None, h0=None, lengths=None, y=None, h_final=None, states=None,

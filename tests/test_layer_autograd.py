@@ -124,3 +124,19 @@ def test_written_tensors_of_inference_mode():
     with torch.inference_mode():
         for _, call, _ in writers():
             call()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(2, 16), (2, 1, 16), (1, 2, 16), (32,)])
+def test_start_state_of_any_shape(shape):
+    """h0 of b d elements in any shape, as the call takes it, gets its gradient in
+    that shape."""
+    from gpu_util import dev
+    gen = torch.Generator().manual_seed(1)
+    v, g, h0 = (torch.randn(*s, generator=gen).to(dev()) for s in ((2, 8, 16), (2, 8, 16), (2, 16)))
+    leaf = h0.reshape(shape).clone().requires_grad_()
+    y, h = api.gated_scan(v, g, h0=leaf)
+    y.sum().backward()
+    st = api.gated_scan(v, g, h0=h0, save_states=True)[2]
+    want = api.gated_scan_backward(torch.ones_like(v), v, g, st)[3]
+    assert leaf.grad.shape == leaf.shape and torch.equal(leaf.grad.reshape(2, 16), want)
