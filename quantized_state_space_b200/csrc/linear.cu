@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kSplitThreads)
 // traffic per MMA of two separate 128 x 256 tiles), the leader issues the
 // MMAs of both.  Accumulators are double-buffered in TMEM (2 x 256 columns),
 // so eight warps per CTA write tile i (through shared memory by TMA, 256-byte rows,
-// where y lies on 16-byte rows) while the MMAs of tile i + 1 run (four were
+// where y's rows are whole 16-byte pieces) while the MMAs of tile i + 1 run (four were
 // slower than the MMAs: 206 against 126 us of MMAs at 16384 x 2560 x 5120).
 // A wait that gives up raises a word in both CTAs.  Each role then ends by itself (no
 // accumulator is handed on that is not complete), the epilogue writes NaN to the tiles
@@ -941,7 +941,8 @@ cudaError_t launch_int8_linear(const ssmq_linear_args& a, void* ws, cudaStream_t
   if (e != cudaSuccess) return e;
   CUtensorMap ymap = {};
   const int esz = p.dtype == SSMQ_F32 ? 4 : 2;
-  if (rows16(p.y, p.ldy, esz) && p.ldy < ((int64_t)1 << 36)) {
+  // (a TMA store writes whole 16-byte pieces of a row: N has to end with one)
+  if (rows16(p.y, p.ldy, esz) && p.N * esz % 16 == 0 && p.ldy < ((int64_t)1 << 36)) {
     const cuuint64_t dims[2] = {(cuuint64_t)p.N, (cuuint64_t)p.M};
     const cuuint64_t strides[1] = {(cuuint64_t)p.ldy * esz};
     const cuuint32_t box[2] = {(cuuint32_t)kRows, esz == 4 ? 64u : 128u};
