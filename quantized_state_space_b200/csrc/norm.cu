@@ -284,8 +284,23 @@ __global__ void __launch_bounds__(kTpr <= 32 ? kSmallThreads : kTpr)
   uint32_t flags = 0;
   const bool good = isfinite(sum);
   const float rstd = rsqrtf(fmaf(sum, p.inv_dim, p.eps));
-  const float amax = mx * rstd;
-  // (eps = 0 and a zero row: 0 * inf; an overflowing maximum has no finite scale)
+  float amax = mx * rstd;
+  // an infinite value of a finite product (in any row of this warp, or in the CTA's
+  // row): the maximum over the finite values
+  if (__any_sync(0xFFFFFFFFu, good && amax > 3.40282347e+38f)) {
+    amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float m = fabsf(v[i][j] * rstd);
+        amax = isfinite(m) ? fmaxf(amax, m) : amax;
+      }
+    if constexpr (!kInWarp) __syncthreads();  // (s_max is read)
+    float none = 0.0f;
+    reduce(none, amax);
+  }
+  // (eps = 0 and a zero row: 0 * inf)
   const float s = good && isfinite(amax) ? __fdiv_rn(amax, 127.0f) : 0.0f;
   const float rs = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
   const bool fast = s > 0.0f && usable_recip(s, rs);
