@@ -684,7 +684,9 @@ ssmq_status ssmq_selective_state_update_w8(const ssmq_m1_decode_args* args, void
  * >= the row's length), so that column slices of a wider tensor need no copy.
  * Base pointers need the alignment of one element (tensors without a stride
  * argument: 4 bytes for fp32 and int32); rows on 16-byte boundaries take
- * vectorised paths with the same results.
+ * vectorised paths with the same results.  Kernels may read, and drop, the other
+ * bytes of the aligned 16 bytes that an input's first or last element lies in
+ * (every device allocation holds them); they write a tensor's own elements only.
  */
 
 /*

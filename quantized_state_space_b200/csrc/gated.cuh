@@ -197,8 +197,8 @@ struct Stage {
     }
     const uint32_t dst = tc::smem_u32(at(buf, tensor));
     if constexpr (kWords) {
-      // words that hold a channel of the row (and the one beside it: the word lies
-      // in the tensor's own memory)
+      // words that hold a channel of the row; the half beside it (another channel, or at
+      // the tensor's ends what lies beside it in that word) is dropped
       const int l = (int)threadIdx.x % kLanes;
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {

@@ -726,7 +726,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
 // ---- rows onto 16-byte boundaries -----------------------------------------------
 // Operands whose base or stride TMA cannot take are copied once to rows of a
 // multiple of 16 bytes (zero-padded): one aligned 16-byte store per thread,
-// its bytes gathered from aligned 32-bit words.
+// its bytes gathered from aligned 32-bit words (whose other bytes are dropped).
 struct AlignJob {
   const int8_t* src;
   int64_t stride, rows;

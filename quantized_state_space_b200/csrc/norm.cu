@@ -73,7 +73,8 @@ enum {
 // w[c8 - mis .. c8 - mis + 7] (c8 a multiple of 8, mis < 8) from the four aligned
 // 16-byte pieces around them, by three stages of selects: eight loads of single
 // weights, 32 bytes apart between lanes, cost four times the cache wavefronts.
-// Indices outside the row read some weight of it.
+// Indices outside the row read some weight of it, or (dim no multiple of 4) the bytes
+// behind the last one in its aligned 16: the caller drops both.
 __device__ __forceinline__ void shifted_weights(const float* w, int c8, int mis, int dim,
                                                 float (&o)[8]) {
   const float4* w4 = reinterpret_cast<const float4*>(w);
@@ -133,8 +134,8 @@ __global__ void __launch_bounds__(kTpr <= 32 ? kSmallThreads : kTpr)
         unpack8<T>(r, o);
       } else if (kMode == kShifted && c > -8 && c < p.dim) {
         // an end of the row: the aligned 16 bytes around it, whose other elements
-        // (the next row's, or padding) are dropped; 16 bytes without an element of
-        // the row are not read
+        // (the next row's, padding, or what lies beside the tensor) are dropped; 16
+        // bytes without an element of the row are not read
         if constexpr (sizeof(T) == 2) {
           const Raw8<T> r = load8(q + c);
           unpack8<T>(r, o);
