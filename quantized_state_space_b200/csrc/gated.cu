@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T
   constexpr int kSteps = TileT::kSteps;
   __shared__ Shared<TileT> sh;
   const uint32_t size = cluster_size(), rank = cluster_rank();
+  uint32_t live = size, limit = p.wait_limit;  // (see carry_in)
   const int64_t unit = blockIdx.x / size;  // (sequence, channel block)
   const int64_t seq = unit / p.blocks, blk = unit % p.blocks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -79,7 +80,7 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T
   St stage(slots);
   __shared__ uint64_t full[St::kBufs];
   const int64_t rounds = (p.tiles + size - 1) / size;
-  uint32_t flags = 0;
+  uint32_t late = 0;  // a wait gave up
   auto fetch = [&](int64_t k) {
     if (k >= rounds) {
       if constexpr (kMode != kTma) St::commit();
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T
     }
     const int buf = (int)(k % St::kBufs);
     if constexpr (kMode == kTma) {
-      if (threadIdx.x == 0 && !flags) {
+      if (threadIdx.x == 0 && !late) {
         const int c = (int)(blk * TileT::kChannels), t = (int)((k * size + rank) * TileT::kLen);
         stream::expect_tx(full + buf, kTensors * St::kTensorBytes);
 #pragma unroll
@@ -113,8 +114,8 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T
   for (int64_t k = 0; k < rounds; ++k) {
     const int buf = (int)(k % St::kBufs);
     if constexpr (kMode == kTma) {
-      if (!flags && !wait_tile(full + buf, (uint32_t)(k / St::kBufs) & 1u, p.wait_limit))
-        flags |= SSMQ_DEV_TIMEOUT;
+      if (!wait_tile(full + buf, (uint32_t)(k / St::kBufs) & 1u, limit))
+        late = 1;
     } else {
       fetch(k + kAhead);
       St::wait();
@@ -141,8 +142,8 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T
       a = fmul2(a, f[i]);
       b = ffma2(f[i], b, u[i]);
     }
-    float2 s = carry_in<TileT, false>(sh, k, make_float4(a.x, a.y, b.x, b.y), h, rank, size,
-                                      p.wait_limit, flags, [&] {
+    float2 s = carry_in<TileT, false>(sh, k, make_float4(a.x, a.y, b.x, b.y), h, rank, live,
+                                      limit, late, [&] {
                                         // (the tile before this one is read: its buffer is free)
                                         if constexpr (kMode == kTma) fetch(k + kAhead);
                                       });
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T
       }
     }
   }
-  if (kMode == kTma && flags && threadIdx.x == 0) {  // the copies in flight land
+  if (kMode == kTma && late && threadIdx.x == 0) {  // the copies in flight land
     const int64_t k = sh.leave_at;
     for (int64_t j = k; j < rounds && j < k + kAhead; ++j)
       wait_tile(full + j % St::kBufs, (uint32_t)(j / St::kBufs) & 1u, kWaitLimit);
@@ -183,8 +184,8 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kScanCtas<T
     if (in0) o[0] = h.x;
     if (in1) o[next] = h.y;
   }
-  flag_status(p.status, flags);
-  carry_done(sh, rounds, size, flags);
+  flag_status(p.status, late ? SSMQ_DEV_TIMEOUT : 0u);
+  carry_done(sh, rounds, late);
 }
 
 template <typename T>

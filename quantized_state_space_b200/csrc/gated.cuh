@@ -394,10 +394,10 @@ __device__ __forceinline__ void carry_init(Shared<TileT>& sh, uint32_t size) {
   }
   cluster_sync();
 }
-// A thread whose wait gives up raises its flags.  At the CTA's next barrier all its
-// threads learn of it (flags != 0 in every one) and leave the exchange: they wait for
-// nothing, fetch and push nothing, and go through the rounds with a NaN state, so that
-// what the CTA has not finished is NaN.  Returns that state.
+// A thread whose wait gives up sets its word `late`.  At the CTA's next barrier all its
+// threads learn of it (the word is set in every one) and leave the exchange: they wait
+// for nothing, fetch and push nothing, and go through the rounds with a NaN state, so
+// that what the CTA has not finished is NaN.  Returns that state.
 template <typename TileT>
 __device__ __forceinline__ float2 leave(Shared<TileT>& sh, int64_t k) {
   if (threadIdx.x == 0 && sh.leave_at == kNever) sh.leave_at = (uint32_t)k;
@@ -409,10 +409,11 @@ __device__ __forceinline__ float2 leave(Shared<TileT>& sh, int64_t k) {
 // the others may have pushed.  (Round k - 2 had arrived before this CTA pushed round
 // k - 1, and nobody pushes round k + 1 without this CTA's round k.)
 template <typename TileT>
-__device__ __forceinline__ void carry_done(Shared<TileT>& sh, int64_t rounds, uint32_t size,
-                                           uint32_t flags) {
+__device__ __forceinline__ void carry_done(Shared<TileT>& sh, int64_t rounds, uint32_t late) {
+  uint32_t size;  // (read anew: no register holds it through the rounds)
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
   if (size == 1) return;
-  if (flags) {
+  if (late) {
     for (uint32_t r = 0; r < size; ++r) store_remote(&sh.left, r, 1u);
     // (cluster_meet orders nothing by itself)
     asm volatile("fence.acq_rel.cluster;" ::: "memory");
@@ -455,12 +456,13 @@ __device__ __forceinline__ void carry_done(Shared<TileT>& sh, int64_t rounds, ui
 // pushes round k + 2 only after it has every map of round k + 1, and a CTA pushes
 // round k + 1 only when its threads are done with round k.  met() runs behind the
 // CTA's barrier: every thread is done with the rounds before this one, and with
-// what it read of this round before the call.  kReverse: flags are the CTA's already
-// (a barrier lies between the round's waits and the call).
+// what it read of this round before the call.  size and limit (of the waits) become 1
+// and 0 where the CTA leaves the exchange.  kReverse: late is the CTA's already (a
+// barrier lies between the round's waits and the call).
 template <typename TileT, bool kReverse, typename Met>
 __device__ __forceinline__ float2 carry_in(Shared<TileT>& sh, int64_t k, float4 m, float2& h,
-                                           uint32_t rank, uint32_t size, uint32_t limit,
-                                           uint32_t& flags, Met met) {
+                                           uint32_t rank, uint32_t& size, uint32_t& limit,
+                                           uint32_t& late, Met met) {
   const int buf = (int)(k & 1);
   constexpr int kSubs = TileT::kSubs, kLanes = TileT::kLanes, kWarps = TileT::kWarps;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -484,8 +486,12 @@ __device__ __forceinline__ float2 carry_in(Shared<TileT>& sh, int64_t k, float4 
   if constexpr (kReverse)
     __syncthreads();
   else
-    flags = __syncthreads_or(flags) ? SSMQ_DEV_TIMEOUT : 0;
-  if (flags) h = leave(sh, k);
+    late = __syncthreads_or(late);
+  if (late) {
+    h = leave(sh, k);
+    size = 1;
+    limit = 0;
+  }
   met();
   float4 pre = make_float4(1.0f, 1.0f, 0.0f, 0.0f), all = pre;
 #pragma unroll
@@ -496,15 +502,14 @@ __device__ __forceinline__ float2 carry_in(Shared<TileT>& sh, int64_t k, float4 
   float2 base = h;
   if (size > 1) {
     // warp i tells CTA i (and i + 8) of the cluster what this CTA's tile does to a state
-    const uint32_t live = flags ? 0 : size;
-    if (threadIdx.x == 0 && !flags)
+    if (threadIdx.x == 0)
       stream::expect_tx(sh.bar + buf, size * kLanes * (uint32_t)sizeof(float4));
     if (sub0 == 0)
-      for (uint32_t r = (uint32_t)warp; r < live; r += kWarps)
+      for (uint32_t r = (uint32_t)warp; r < size; r += kWarps)
         push_f4(&sh.cta[buf][rank][l], sh.bar + buf, r, all);
     float2 s = h;
-    if (!wait_cluster(sh.bar + buf, (uint32_t)(k >> 1) & 1u, flags ? 0 : limit)) {
-      flags |= SSMQ_DEV_TIMEOUT;
+    if (!wait_cluster(sh.bar + buf, (uint32_t)(k >> 1) & 1u, limit)) {
+      late = 1;
       s = base = nan2();
     }
     __syncwarp();

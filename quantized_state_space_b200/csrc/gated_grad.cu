@@ -47,6 +47,7 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kGradCtas)
   __shared__ Shared<TileT> sh;
   __shared__ float4 s_fwd[2][TileT::kWarps][kLanes];
   const uint32_t size = cluster_size(), rank = cluster_rank();
+  uint32_t live = size, limit = p.wait_limit;  // (see carry_in)
   const int64_t unit = blockIdx.x / size;
   const int64_t seq = unit / p.blocks, blk = unit % p.blocks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -86,14 +87,14 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kGradCtas)
   stage.channels = (int)(p.d - block < TileT::kChannels ? p.d - block : TileT::kChannels);
   __shared__ uint64_t full[St::kBufs];
   const int64_t rounds = (p.tiles + size - 1) / size;
-  uint32_t flags = 0;
+  uint32_t late = 0;  // a wait gave up
   // tiles from the last one backwards; rank 0 holds the latest of a round
   auto tile_of = [&](int64_t k) { return p.tiles - 1 - (k * size + rank); };
   auto fetch = [&](int64_t k) {
     const int64_t tile = tile_of(k);
     const int buf = (int)(k % St::kBufs);
     if constexpr (kMode == kTma) {
-      if (threadIdx.x == 0 && !flags && k < rounds && tile >= 0) {
+      if (threadIdx.x == 0 && !late && k < rounds && tile >= 0) {
         const int c = (int)(blk * TileT::kChannels), t = (int)(tile * TileT::kLen);
         stream::expect_tx(full + buf, (kGate ? 4 : 3) * St::kTensorBytes);
 #pragma unroll
@@ -132,9 +133,8 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kGradCtas)
       hs = make_float2(sp[0], sp[next]);
     }
     if constexpr (kMode == kTma) {
-      if (real && !flags &&
-          !wait_tile(full + buf, (uint32_t)(k / St::kBufs) & 1u, p.wait_limit))
-        flags |= SSMQ_DEV_TIMEOUT;
+      if (real && !wait_tile(full + buf, (uint32_t)(k / St::kBufs) & 1u, limit))
+        late = 1;
       if (left < kSteps) stage.clear(buf, left);
     } else {
       St::wait();
@@ -174,8 +174,8 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kGradCtas)
         const float4 before = shfl_f4(m, (lane - kLanes) & 31);
         if (sub > 0) mine = before;
       }
-      flags = __syncthreads_or(flags) ? SSMQ_DEV_TIMEOUT : 0;
-      if (flags) hs = nan2();  // (dz goes out next)
+      late = __syncthreads_or(late);
+      if (late) hs = nan2();  // (dz goes out next)
 #pragma unroll
       for (int w = 0; w < TileT::kWarps - 1; ++w) {
         const float4 e = s_fwd[k & 1][w][l];
@@ -213,8 +213,8 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kGradCtas)
     float2 r = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = kSteps - 1; i >= 0; --i) r = fmul2(f[i], fadd2(dh[i], r));
-    r = carry_in<TileT, true>(sh, k, make_float4(a.x, a.y, r.x, r.y), c, rank, size,
-                              p.wait_limit, flags, [&] {
+    r = carry_in<TileT, true>(sh, k, make_float4(a.x, a.y, r.x, r.y), c, rank, live, limit, late,
+                              [&] {
                                 fetch(k + St::kBufs);  // (every thread has read this tile)
                               });
     T* dvo = dvp + (t0 + kSteps - 1) * p.dv.rs;
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kGradCtas)
       for (int i = kSteps - 1; i >= 0; --i) put(i, i < left, t0 + i < p.L);
     }
   }
-  if (kMode == kTma && flags && threadIdx.x == 0) {  // the copies in flight land
+  if (kMode == kTma && late && threadIdx.x == 0) {  // the copies in flight land
     const int64_t k = sh.leave_at;
     for (int64_t j = k; j < rounds && j < k + St::kBufs && tile_of(j) >= 0; ++j)
       wait_tile(full + j % St::kBufs, (uint32_t)(j / St::kBufs) & 1u, kWaitLimit);
@@ -251,8 +251,8 @@ __global__ void __launch_bounds__(ModeTile<kMode, kLanes>::kThreads, kGradCtas)
     if (in0) o[0] = c.x;
     if (in1) o[next] = c.y;
   }
-  flag_status(p.status, flags);
-  carry_done(sh, rounds, size, flags);
+  flag_status(p.status, late ? SSMQ_DEV_TIMEOUT : 0u);
+  carry_done(sh, rounds, late);
 }
 
 template <typename T>
