@@ -662,9 +662,9 @@ def _written(*tensors):
     """The call has written these tensors of its caller (None: it made its own):
     autograd's version of each counts on, so that a backward pass that saved one
     of them raises instead of using the new contents."""
-    given = [t for t in tensors if t is not None]
-    if given:
-        increment_version(given)
+    for t in tensors:
+        if t is not None:
+            increment_version(t)
 
 
 def _cuda(t, name, dim=None):
@@ -1000,7 +1000,10 @@ def gated_update(state, v, g, *, z=None, y=None):
     v, g, z (b, d) with contiguous channels.  Returns y (b, d) in v's dtype
     (y may be z itself).  There is no gradient (gated_scan has one): tensors
     that require one are refused."""
-    _no_gradient("gated_update", state, v, g, z, y)
+    if (forward_ad._current_level >= 0 or torch.is_grad_enabled() and (
+            v.requires_grad or g.requires_grad or (state is not None and state.requires_grad) or
+            (z is not None and z.requires_grad) or (y is not None and y.requires_grad))):
+        _no_gradient("gated_update", state, v, g, z, y)
     dv, kind = _cuda(v, "v", 2)
     shape, dt = v.shape, v.dtype
     b, d = shape
@@ -1021,5 +1024,7 @@ def gated_update(state, v, g, *, z=None, y=None):
         else:
             rows += _NONE
     _call(dv, N.ssmq_gated_update, b, 1, d, kind, *rows, 0, hp, 0, 0, 0)
-    _written(state, given)
+    increment_version(state)
+    if given is not None:
+        increment_version(given)
     return y
