@@ -101,7 +101,7 @@ struct Maps {
 // own steps and channels.  kDirect: copies of 16-bit channels and of pairs go
 // through registers, not as asynchronous copies of 4 bytes, which the forward kernel
 // with its many warps does not need (8 x 2048 x 1538 binary16, gated: 108 us against
-// 72; odd rows, 1537: 108 against 84; the gradient's odd rows: 188 against 234).
+// 67; odd rows, 1537: 108 against 84; the gradient's odd rows: 188 against 234).
 template <typename T, int kTensors, int kMode, typename TileT, int kBufs_, bool kDirect>
 struct Stage {
   static constexpr int kThreads = TileT::kThreads, kSteps = TileT::kSteps;
